@@ -13,8 +13,10 @@
  * pa_paged_decode_shared_prefix (groups that share a stored prefix read it
  * once), the _fp8 and _int8 variants over one-byte K/V pools (one scale per
  * pool, or one per row with the _rowscale calls), pa_swap_blocks
- * (block copies between device and pinned host pools), and the size
- * queries.  The host block manager that hands out the block ids is declared
+ * (block copies between device and pinned host pools), pa_rope_append (the
+ * cache write with the norms and the position rotation of queries and keys
+ * on the way), the pa_latent_* calls (append, decode and prompt attention
+ * over a paged pool of shared latent rows), and the size queries.  The host block manager that hands out the block ids is declared
  * in pa_block_manager.h.
  *
  * Pages cited (title, then section):
@@ -75,7 +77,10 @@
  *                          a source in the same call (those blocks' contents
  *                          are unspecified);
  *   PA_STATUS_TIMEOUT      a bounded wait for an asynchronous copy gave up
- *                          (should never happen; the output is unspecified).
+ *                          (should never happen; the output is unspecified);
+ *   PA_STATUS_BAD_POSITION a position at or beyond max_position in a rotating
+ *                          append (nothing of the token is written; negative
+ *                          positions are padding and are skipped silently).
  */
 #ifndef PA_H_
 #define PA_H_
@@ -117,6 +122,7 @@ typedef enum pa_dtype {
 #define PA_STATUS_BAD_CONTEXT 4
 #define PA_STATUS_COPY_CONFLICT 8
 #define PA_STATUS_TIMEOUT 16
+#define PA_STATUS_BAD_POSITION 32
 
 /*
  * pa_reshape_and_cache -- write each new token's K and V rows into its slot.
@@ -596,6 +602,160 @@ PA_API pa_status pa_paged_decode_no_alloc(void* out, const void* query, const vo
                                           int32_t max_context_len, float scale,
                                           int32_t partition_size, pa_dtype dtype,
                                           int32_t* d_status, pa_stream_t stream);
+
+/*
+ * pa_rope_append -- the cache write with the norm and the position rotation
+ * of queries and keys in the same pass: what stands between a layer's
+ * projections and pa_paged_decode.
+ *
+ * For token t at position p = positions[t], for every query head and every
+ * key head, with x the head's row (head_dim = D elements) in fp32:
+ *   n(x)   = x * rsqrt(mean(x^2) + eps) * weight      (x itself if weight is NULL)
+ *   rot(x) : the first rot_dim elements in rot_dim / 2 pairs, pair i turned by
+ *            (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i); pair i is
+ *            elements (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved;
+ *            the elements from rot_dim on are kept
+ *   query_out[t][h]    = rot(n(query[t][h]))
+ *   k_cache[slot][g]   = rot(n(key[t][g])),   v_cache[slot][g] = value[t][g]
+ * with slot = slot_mapping[t].  Every result is rounded once, from fp32, to
+ * its stored type.  One-byte pools are written as pa_reshape_and_cache_fp8 /
+ * _int8 (k_scale, v_scale) or, with scale pools, as the _rowscale calls do,
+ * from the fp32 values.
+ *
+ * query          [num_tokens] rows of [num_q_heads][D], query_stride elements
+ *                apart; key, value likewise ([num_kv_heads][D]): slices of one
+ *                fused projection are taken as they are.  Strides are
+ *                multiples of 8 elements and at least a row.
+ * query_out      rows as query, query_out_stride apart; may be query itself.
+ * k_cache, v_cache  pools [num_blocks][block_size][num_kv_heads][D] of
+ *                pool_dtype: `dtype`, PA_DTYPE_FP8_E4M3 or PA_DTYPE_INT8.
+ * k_scales, v_scales  NULL, or the fp32 scale pools [num_blocks][num_kv_heads]
+ *                [block_size] of row-scaled one-byte pools.
+ * slot_mapping   int64; a negative slot: the token's key and value are not
+ *                stored (its queries are still rotated).  The slots of a call
+ *                must be distinct (else that slot's contents are unspecified).
+ * positions      int64; negative = padding token, nothing of it is written.
+ * cos_sin        fp32 [max_position][rot_dim]: rot_dim / 2 cosines, then as
+ *                many sines.  16-byte aligned; may be NULL if rot_dim is 0.
+ * q_weight, k_weight  [D] of `dtype`, or NULL.  eps finite, not negative.
+ * rot_dim        0 .. D, a multiple of 16 (else PA_ERR_UNSUPPORTED).
+ * d_status       optional; PA_STATUS_BAD_SLOT (the queries are still
+ *                written), PA_STATUS_BAD_POSITION.
+ */
+PA_API pa_status pa_rope_append(
+    void* query_out, const void* query, const void* key, const void* value, void* k_cache,
+    void* v_cache, float* k_scales, float* v_scales, const int64_t* slot_mapping,
+    const int64_t* positions, const float* cos_sin, const void* q_weight, const void* k_weight,
+    float eps, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t rot_dim, int64_t max_position, int32_t interleaved, int64_t query_out_stride,
+    int64_t query_stride, int64_t key_stride, int64_t value_stride, int32_t block_size,
+    int64_t num_blocks, pa_dtype dtype, pa_dtype pool_dtype, float k_scale, float v_scale,
+    int32_t* d_status, pa_stream_t stream);
+
+/*
+ * Latent KV cache -- attention whose keys and values of every head come from
+ * one shared latent vector a token.  The pool holds, for each token, one row
+ * of latent_dim elements c (the latent vector) followed by rope_dim elements
+ * r (a key part shared by the heads, already rotated):
+ *   cache : [num_blocks][block_size][latent_dim + rope_dim], 16-bit,
+ * reached through block tables as the K / V pools are.  With the up-projection
+ * w_kv [num_heads][nope_dim + value_dim][latent_dim] the key and value of
+ * head h at a token are
+ *   K = (w_kv[h][:nope_dim] c, r),   V = w_kv[h][nope_dim:] c.
+ * latent_dim 256 or 512, rope_dim 64, block_size 8, 16, 32 or 64, num_heads
+ * at most 128, F16 or BF16 (else PA_ERR_UNSUPPORTED).
+ *
+ * pa_latent_append -- write each token's row to its slot, normalised and
+ * rotated on the way, and rotate the queries' rotated part:
+ *   cache[slot] = (n(latent[t][:latent_dim]), rot(latent[t][latent_dim:]))
+ *   query_out[t][h] = rot(query_rope[t][h])
+ * with n and rot (rot_dim = rope_dim) of pa_rope_append.
+ *
+ * latent         rows [latent_dim + rope_dim], latent_stride elements apart.
+ * query_rope, query_out  [num_tokens][num_heads][rope_dim] with strides in
+ *                elements between tokens and between heads (the tail of each
+ *                head's query row); query_out may be query_rope itself.
+ *                num_heads 0: no queries (the pointers may be NULL).
+ * weight         [latent_dim] of `dtype`, or NULL: no norm.
+ * Other arguments, padding and status bits as pa_rope_append.
+ */
+PA_API pa_status pa_latent_append(
+    void* query_out, const void* query_rope, const void* latent, void* cache,
+    const int64_t* slot_mapping, const int64_t* positions, const float* cos_sin,
+    const void* weight, float eps, int32_t num_tokens, int32_t num_heads, int32_t latent_dim,
+    int32_t rope_dim, int64_t max_position, int32_t interleaved, int64_t query_out_stride,
+    int64_t query_out_head_stride, int64_t query_stride, int64_t query_head_stride,
+    int64_t latent_stride, int32_t block_size, int64_t num_blocks, pa_dtype dtype,
+    int32_t* d_status, pa_stream_t stream);
+
+/*
+ * pa_latent_decode -- one query a sequence over the latent pool, with the
+ * projections absorbed: the caller's query holds w_kv[h][:nope_dim]^T q_nope
+ * (latent_dim elements) followed by the rotated part, and the output is the
+ * weighted sum of latent vectors, to which w_kv[h][nope_dim:] is applied
+ * afterwards.  For row_t the pool's row of token t < context_lens[s]:
+ *   x_t = scale * sum_d query[s][h][d] * row_t[d]
+ *   out[s][h][:] = sum_t softmax(x)_t * row_t[:latent_dim]
+ *
+ * out            [num_seqs][num_heads][latent_dim], 16-byte aligned; written.
+ * query          [num_seqs][num_heads][latent_dim + rope_dim], 16-byte aligned.
+ * workspace      at least pa_latent_decode_workspace_size(...) bytes, 16-byte
+ *                aligned (may be NULL when that is 0); its contents on entry
+ *                do not matter; calls that share it must not overlap.
+ * Products take 16-bit operands with fp32 sums; softmax statistics are fp32.
+ * Other arguments, empty and bad contexts, bad blocks, the order of sums and
+ * status bits as pa_paged_decode.
+ */
+PA_API size_t pa_latent_decode_workspace_size(int32_t num_seqs, int32_t num_heads,
+                                              int32_t latent_dim, int32_t block_size,
+                                              int32_t max_context_len);
+
+PA_API pa_status pa_latent_decode(void* out, const void* query, const void* cache,
+                                  const int32_t* block_tables, const int32_t* context_lens,
+                                  int32_t num_seqs, int32_t num_heads, int32_t latent_dim,
+                                  int32_t rope_dim, int32_t block_size, int32_t max_blocks_per_seq,
+                                  int64_t num_blocks, int32_t max_context_len, float scale,
+                                  void* workspace, size_t workspace_bytes, pa_dtype dtype,
+                                  int32_t* d_status, pa_stream_t stream);
+
+/*
+ * pa_latent_prefill -- the new tokens of each sequence over the latent pool,
+ * with keys and values expanded.  Sequence s has query rows
+ * [query_starts[s], query_starts[s + 1]) and context_lens[s] tokens in the
+ * pool, its new ones last (append them first); query i of n attends to the
+ * tokens at positions up to context_lens[s] - n + i:
+ *   x_t = scale * (q_nope . K_nope_t + q_rope . r_t),
+ *   out = sum_t softmax(x)_t V_t.
+ *
+ * out            [num_tokens][num_heads][value_dim], 16-byte aligned; written
+ *                for the rows of the sequences, others are left as they were.
+ * query          [num_tokens][num_heads][nope_dim + rope_dim] (rotated).
+ * w_kv           [num_heads][nope_dim + value_dim][latent_dim], contiguous.
+ * query_starts   int32 [num_seqs + 1], not decreasing, at most num_tokens.
+ * max_query_len, max_context_len  host upper bounds (they size the grids and
+ *                the workspace).
+ * nope_dim, value_dim  128 (else PA_ERR_UNSUPPORTED).
+ * workspace      at least pa_latent_prefill_workspace_size(...) bytes, 16-byte
+ *                aligned: K and V of every head, 16-bit, max_context_len rows a
+ *                sequence.  Contents on entry do not matter; calls that share
+ *                it must not overlap.
+ * d_status       optional; PA_STATUS_BAD_CONTEXT: query_starts that decrease,
+ *                pass num_tokens or exceed max_query_len (the sequence's rows
+ *                are left as they were), a context that pa_paged_decode
+ *                refuses or that is shorter than the sequence's new tokens
+ *                (zero rows); PA_STATUS_BAD_BLOCK, PA_STATUS_TIMEOUT.
+ */
+PA_API size_t pa_latent_prefill_workspace_size(int32_t num_seqs, int32_t num_heads,
+                                               int32_t latent_dim, int32_t block_size,
+                                               int32_t max_context_len);
+
+PA_API pa_status pa_latent_prefill(
+    void* out, const void* query, const void* cache, const void* w_kv, const int32_t* block_tables,
+    const int32_t* query_starts, const int32_t* context_lens, int32_t num_seqs, int32_t num_tokens,
+    int32_t num_heads, int32_t latent_dim, int32_t rope_dim, int32_t nope_dim, int32_t value_dim,
+    int32_t block_size, int32_t max_blocks_per_seq, int64_t num_blocks, int32_t max_query_len,
+    int32_t max_context_len, float scale, void* workspace, size_t workspace_bytes, pa_dtype dtype,
+    int32_t* d_status, pa_stream_t stream);
 
 /* Human-readable name of a pa_status (static string, never NULL). */
 PA_API const char* pa_status_string(pa_status status);

@@ -17,6 +17,13 @@ inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7
 inline bool supported_head_dim(int32_t d) { return d == 64 || d == 128; }
 inline bool supported_block_size(int32_t b) { return b == 8 || b == 16 || b == 32; }
 inline bool supported_dtype(int32_t t) { return t == PA_DTYPE_F16 || t == PA_DTYPE_BF16; }
+// Latent pools: rows of latent_dim shared elements and rope_dim rotated ones.
+inline bool supported_latent(int32_t latent_dim, int32_t rope_dim)
+{
+    return (latent_dim == 256 || latent_dim == 512) && rope_dim == 64;
+}
+constexpr int32_t kMaxLatentHeads = 128;
+inline bool supported_latent_block(int32_t b) { return supported_block_size(b) || b == 64; }
 // One-byte pool element types (block copies and swaps move them as bytes).
 inline bool code_dtype(int32_t t) { return t == PA_DTYPE_FP8_E4M3 || t == PA_DTYPE_INT8; }
 

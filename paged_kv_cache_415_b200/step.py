@@ -16,6 +16,11 @@ scales.  ``run_from_host`` is the same step fed from pinned host buffers: it
 copies the step's inputs to the device, runs the step and copies the output
 back, all on the same stream.
 
+A step given a ``Rotation`` and positions takes queries and keys as the
+layer's projections leave them: ``pa_rope_append`` normalises and rotates
+them on the way into the pools.  ``LatentDecodeStep`` is the same step over a
+pool of latent rows (``pa_latent_append``, then ``pa_latent_decode``).
+
 Tracing: every step and each of its calls is an NVTX range on the host
 thread that issues it ("pa.step", "pa.copy_blocks", "pa.cache_write",
 "pa.decode"; in ``HostPipeline`` also "pa.upload" and "pa.download"), so a
@@ -39,6 +44,18 @@ _QUANTISED_CALLS = {
     torch.int8: ("pa_reshape_and_cache_int8", "pa_paged_decode_int8",
                  "pa_paged_decode_int8_append"),
 }
+
+
+class Rotation:
+    """How a layer's queries and keys become what its pools hold: the angle
+    table cos_sin (fp32 [max_position][rot_dim], cosines then sines), the
+    optional norm weights [D] of queries and keys, eps, and whether a pair is
+    two adjacent elements (interleaved) or one of each half."""
+
+    def __init__(self, cos_sin: torch.Tensor, q_weight: torch.Tensor = None,
+                 k_weight: torch.Tensor = None, eps: float = 1e-6, interleaved: bool = False):
+        self.cos_sin, self.q_weight, self.k_weight = cos_sin, q_weight, k_weight
+        self.eps, self.interleaved = float(eps), bool(interleaved)
 
 
 class DecodeStep:
@@ -72,25 +89,48 @@ class DecodeStep:
         dev = k_cache.device
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None
         self.d_status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._rotated = None              # the rotated queries of steps with a Rotation
 
     def __call__(self, query, block_tables, context_lens, scale, out=None, new_key=None,
                  new_value=None, slot_mapping=None, block_mapping=None, stream=None,
-                 max_context_len=None, fused_append=False):
+                 max_context_len=None, fused_append=False, positions=None, rotation=None):
         """fused_append: every sequence appends exactly one token (new_key /
         new_value hold one row per sequence, at position context_lens - 1);
         the cache write then runs inside the decode launch
-        (pa_paged_decode_append) and slot_mapping is not used."""
+        (pa_paged_decode_append) and slot_mapping is not used.
+        rotation (a Rotation) with positions (int64 [num_seqs]): query and
+        new_key are rotated (and normalised) by pa_rope_append, which also
+        does the cache write at slot_mapping; query itself is left as it is.
+        It takes the place of the cache write, so not with fused_append."""
         with _range("pa.step"):
             return self._step(query, block_tables, context_lens, scale, out, new_key, new_value,
-                              slot_mapping, block_mapping, stream, max_context_len, fused_append)
+                              slot_mapping, block_mapping, stream, max_context_len, fused_append,
+                              positions, rotation)
+
+    def _rotate(self, query, new_key, new_value, slot_mapping, positions, rotation, stream):
+        """pa_rope_append into the pools; returns the rotated queries, in a
+        buffer that the next rotating step reuses."""
+        if self._rotated is None or self._rotated.shape != query.shape \
+                or self._rotated.dtype != query.dtype:
+            self._rotated = torch.empty(query.shape, dtype=query.dtype, device=query.device)
+        with _range("pa.cache_write"):
+            B.pa_rope_append(self._rotated, query, new_key, new_value, self.k_cache, self.v_cache,
+                             slot_mapping, positions, rotation.cos_sin, rotation.q_weight,
+                             rotation.k_weight, rotation.eps, rotation.interleaved, self.k_scale,
+                             self.v_scale, self.k_scales, self.v_scales, self.d_status, stream)
+        return self._rotated
 
     def _step(self, query, block_tables, context_lens, scale, out, new_key, new_value,
-              slot_mapping, block_mapping, stream, max_context_len, fused_append):
+              slot_mapping, block_mapping, stream, max_context_len, fused_append, positions,
+              rotation):
+        if rotation is not None and (fused_append or positions is None or slot_mapping is None):
+            raise ValueError("a step with a rotation needs positions and slot_mapping, and does "
+                             "not fuse its append into the decode")
         if block_mapping is not None and block_mapping.shape[0] > 0:
             with _range("pa.copy_blocks"):
                 B.pa_copy_blocks(self.k_cache, self.v_cache, block_mapping, self.d_status, stream)
         if out is None:
-            out = torch.empty_like(query)
+            out = torch.empty(query.shape, dtype=query.dtype, device=query.device)
         mcl = self.max_context_len if max_context_len is None else max_context_len
         write_needed = slot_mapping is not None and slot_mapping.shape[0] > 0
         if self.quantised is not None and self.k_scales is not None:
@@ -105,7 +145,10 @@ class DecodeStep:
                                   vs, block_tables, context_lens, mcl, scale, self.partition_size,
                                   self.workspace, self.d_status, stream)
                 return out
-            if write_needed:
+            if rotation is not None:
+                query = self._rotate(query, new_key, new_value, slot_mapping, positions, rotation,
+                                     stream)
+            elif write_needed:
                 with _range("pa.cache_write"):
                     write(new_key, new_value, self.k_cache, self.v_cache, ks, vs, slot_mapping,
                           self.d_status, stream)
@@ -122,7 +165,10 @@ class DecodeStep:
                                   self.v_scale, self.partition_size, self.workspace,
                                   self.d_status, stream)
                 return out
-            if write_needed:
+            if rotation is not None:
+                query = self._rotate(query, new_key, new_value, slot_mapping, positions, rotation,
+                                     stream)
+            elif write_needed:
                 with _range("pa.cache_write"):
                     write(new_key, new_value, self.k_cache, self.v_cache, slot_mapping,
                           self.k_scale, self.v_scale, self.d_status, stream)
@@ -138,7 +184,10 @@ class DecodeStep:
                                          self.partition_size, self.workspace, self.d_status,
                                          stream)
             return out
-        if write_needed:
+        if rotation is not None:
+            query = self._rotate(query, new_key, new_value, slot_mapping, positions, rotation,
+                                 stream)
+        elif write_needed:
             with _range("pa.cache_write"):
                 B.pa_reshape_and_cache(new_key, new_value, self.k_cache, self.v_cache,
                                        slot_mapping, self.d_status, stream)
@@ -149,14 +198,16 @@ class DecodeStep:
         return out
 
     def graph(self, query, block_tables, context_lens, scale, out, new_key=None, new_value=None,
-              slot_mapping=None, block_mapping=None, fused_append=False):
+              slot_mapping=None, block_mapping=None, fused_append=False, positions=None,
+              rotation=None):
         """Capture one step on these device buffers into a CUDA graph and
         return it (``torch.cuda.CUDAGraph``); ``replay()`` re-runs the step's
         launches with no host work per launch.  The step runs once eagerly on
         a side stream first, so every per-kernel setting is in place before
         capture.  Refill the captured buffers in place between replays."""
         args = dict(out=out, new_key=new_key, new_value=new_value, slot_mapping=slot_mapping,
-                    block_mapping=block_mapping, fused_append=fused_append)
+                    block_mapping=block_mapping, fused_append=fused_append, positions=positions,
+                    rotation=rotation)
         side = torch.cuda.Stream(device=query.device)
         side.wait_stream(torch.cuda.current_stream(query.device))
         with torch.cuda.stream(side):
@@ -185,6 +236,51 @@ class DecodeStep:
                  stream=s, fused_append=fused_append)
             host["out"].copy_(dev["out"], non_blocking=True)
         return host["out"]
+
+
+class LatentDecodeStep:
+    """One decode step of one layer over a paged pool of latent rows:
+
+        latent_append(new rows, queries' rotated part)   into the slots
+        latent_decode(query, ...)                        the new tokens included
+
+    The workspace and the status word are allocated once; a step's calls run
+    on one stream."""
+
+    def __init__(self, cache: torch.Tensor, num_seqs: int, num_heads: int, max_context_len: int,
+                 rope_dim: int = 64):
+        self.cache = cache
+        _, self.block_size, width = cache.shape
+        self.latent_dim, self.rope_dim = width - rope_dim, rope_dim
+        self.num_heads, self.max_context_len = num_heads, max_context_len
+        n = B.pa_latent_decode_workspace_size(num_seqs, num_heads, self.latent_dim,
+                                              self.block_size, max_context_len)
+        dev = cache.device
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        self.d_status = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def __call__(self, query, block_tables, context_lens, scale, out=None, new_latent=None,
+                 slot_mapping=None, positions=None, cos_sin=None, weight=None, eps=1e-6,
+                 interleaved=False, stream=None):
+        """query [S][H][L + R]: the absorbed part, then the part that is
+        rotated in place by the angles of `positions` when new_latent [S][L +
+        R], the step's new rows, is given (they go to slot_mapping, the latent
+        part normalised by `weight`).  Without new_latent the query is taken
+        as rotated.  Returns out [S][H][L]."""
+        with _range("pa.step"):
+            if new_latent is not None:
+                tail = query[..., self.latent_dim:]
+                with _range("pa.cache_write"):
+                    B.pa_latent_append(tail, tail, new_latent, self.cache, slot_mapping, positions,
+                                       cos_sin, weight, eps, interleaved, self.d_status, stream)
+            if out is None:
+                out = torch.empty(*query.shape[:2], self.latent_dim, dtype=query.dtype,
+                                  device=query.device)
+            with _range("pa.decode"):
+                B.pa_latent_decode(out, query, self.cache, block_tables, context_lens,
+                                   self.max_context_len, scale, self.workspace, self.d_status,
+                                   stream)
+            return out
 
 
 class HostPipeline:
