@@ -1,10 +1,5 @@
-// latent_attention.cu -- attention over a paged pool of latent rows: each
-// token has one row of latent_dim shared elements c and 64 rotated ones r,
-// from which every head's key and value follow.
-//   pa_latent_decode    absorbed form: the projections are folded into the
-//                       query and the output, so the row is key (all of it)
-//                       and value (its latent part) of every head
-//   pa_latent_prefill   expanded form: K = (W_k c, r), V = W_v c a head
+// latent_prefill.cu -- prompt attention over the paged latent pool with keys
+// and values expanded for each head.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -107,26 +102,6 @@ __device__ void attend_rows(const LatentArgs& a, int s, int32_t seen, const floa
 }
 
 template <typename T, int L>
-__global__ void __launch_bounds__(128) latent_decode_simple_kernel(const LatentArgs a)
-{
-    __shared__ float q[L + 64], result[L], merge[kRowWarps4 * (L + 2)];
-    grid_dependency_wait();
-    const int h = blockIdx.x, s = blockIdx.y;
-    const int64_t row = static_cast<int64_t>(s) * a.num_heads + h;
-    int32_t ctx = a.context_lens[s];
-    if (!good_context(a, ctx)) {
-        if (threadIdx.x == 0) status_or(a.d_status, PA_STATUS_BAD_CONTEXT);
-        ctx = 0;
-    }
-    for (int i = threadIdx.x; i < L + 64; i += blockDim.x)
-        q[i] = lat_to_float(static_cast<const T*>(a.query)[row * (L + 64) + i]);
-    __syncthreads();
-    attend_rows<T, L>(a, s, ctx, q, result, merge);
-    for (int i = threadIdx.x; i < L; i += blockDim.x)
-        lat_store(static_cast<T*>(a.out) + row * L + i, result[i]);
-}
-
-template <typename T, int L>
 __global__ void __launch_bounds__(128) latent_prefill_simple_kernel(const LatentArgs a)
 {
     __shared__ float qin[kNope], q[L + 64], result[L], merge[kRowWarps4 * (L + 2)];
@@ -162,75 +137,14 @@ __global__ void __launch_bounds__(128) latent_prefill_simple_kernel(const Latent
     }
 }
 
-static bool bad_shape(int32_t num_seqs, int32_t num_heads, int32_t latent_dim, int32_t block_size,
-                      int32_t max_context_len)
-{
-    return num_seqs < 0 || num_heads <= 0 || latent_dim <= 0 || block_size <= 0 ||
-           max_context_len < 0;
-}
-
 }  // namespace pa
-
-extern "C" size_t pa_latent_decode_workspace_size(int32_t num_seqs, int32_t num_heads,
-                                                  int32_t latent_dim, int32_t block_size,
-                                                  int32_t max_context_len)
-{
-    return 0;
-}
-
-extern "C" pa_status pa_latent_decode(void* out, const void* query, const void* cache,
-                                      const int32_t* block_tables, const int32_t* context_lens,
-                                      int32_t num_seqs, int32_t num_heads, int32_t latent_dim,
-                                      int32_t rope_dim, int32_t block_size,
-                                      int32_t max_blocks_per_seq, int64_t num_blocks,
-                                      int32_t max_context_len, float scale, void* workspace,
-                                      size_t workspace_bytes, pa_dtype dtype, int32_t* d_status,
-                                      pa_stream_t stream)
-{
-    using namespace pa;
-    if (bad_shape(num_seqs, num_heads, latent_dim, block_size, max_context_len) || rope_dim <= 0 ||
-        max_blocks_per_seq <= 0 || num_blocks <= 0 || !isfinite(scale))
-        return PA_ERR_INVALID_ARG;
-    if (!supported_dtype(dtype) || !supported_latent(latent_dim, rope_dim) ||
-        !supported_latent_block(block_size) || num_heads > kMaxLatentHeads || num_seqs > 65535)
-        return PA_ERR_UNSUPPORTED;
-    if (!out || !query || !cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
-    if (!aligned16(out) || !aligned16(query) || !aligned16(cache) || !aligned4(block_tables) ||
-        !aligned4(context_lens) || (d_status && !aligned4(d_status)))
-        return PA_ERR_INVALID_ARG;
-    const size_t need = pa_latent_decode_workspace_size(num_seqs, num_heads, latent_dim, block_size,
-                                                        max_context_len);
-    if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
-        return PA_ERR_INVALID_ARG;
-    if (num_seqs == 0) return PA_OK;
-    LatentArgs a = {};
-    a.out = out;
-    a.query = query;
-    a.cache = cache;
-    a.block_tables = block_tables;
-    a.context_lens = context_lens;
-    a.num_seqs = num_seqs;
-    a.num_heads = num_heads;
-    a.block_size = block_size;
-    a.max_blocks_per_seq = max_blocks_per_seq;
-    a.num_blocks = num_blocks;
-    a.max_context_len = max_context_len;
-    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    a.d_status = d_status;
-    auto kernel = dtype == PA_DTYPE_F16
-                      ? (latent_dim == 512 ? latent_decode_simple_kernel<__half, 512>
-                                           : latent_decode_simple_kernel<__half, 256>)
-                      : (latent_dim == 512 ? latent_decode_simple_kernel<__nv_bfloat16, 512>
-                                           : latent_decode_simple_kernel<__nv_bfloat16, 256>);
-    return launch_overlapped(kernel, dim3(num_heads, num_seqs), dim3(128), 0, stream, a);
-}
 
 extern "C" size_t pa_latent_prefill_workspace_size(int32_t num_seqs, int32_t num_heads,
                                                    int32_t latent_dim, int32_t block_size,
                                                    int32_t max_context_len)
 {
     using namespace pa;
-    if (bad_shape(num_seqs, num_heads, latent_dim, block_size, max_context_len) ||
+    if (bad_latent_shape(num_seqs, num_heads, latent_dim, block_size, max_context_len) ||
         !supported_latent(latent_dim, 64) || !supported_latent_block(block_size) ||
         num_heads > kMaxLatentHeads)
         return 0;
@@ -247,7 +161,7 @@ extern "C" pa_status pa_latent_prefill(
     int32_t* d_status, pa_stream_t stream)
 {
     using namespace pa;
-    if (bad_shape(num_seqs, num_heads, latent_dim, block_size, max_context_len) || rope_dim <= 0 ||
+    if (bad_latent_shape(num_seqs, num_heads, latent_dim, block_size, max_context_len) || rope_dim <= 0 ||
         nope_dim <= 0 || value_dim <= 0 || num_tokens < 0 || max_query_len < 0 ||
         max_blocks_per_seq <= 0 || num_blocks <= 0 || !isfinite(scale))
         return PA_ERR_INVALID_ARG;

@@ -24,6 +24,12 @@ inline bool supported_latent(int32_t latent_dim, int32_t rope_dim)
 }
 constexpr int32_t kMaxLatentHeads = 128;
 inline bool supported_latent_block(int32_t b) { return supported_block_size(b) || b == 64; }
+inline bool bad_latent_shape(int32_t num_seqs, int32_t num_heads, int32_t latent_dim, int32_t block_size,
+                      int32_t max_context_len)
+{
+    return num_seqs < 0 || num_heads <= 0 || latent_dim <= 0 || block_size <= 0 ||
+           max_context_len < 0;
+}
 // One-byte pool element types (block copies and swaps move them as bytes).
 inline bool code_dtype(int32_t t) { return t == PA_DTYPE_FP8_E4M3 || t == PA_DTYPE_INT8; }
 

@@ -1,0 +1,82 @@
+// pa_tensor_map.h -- host helpers of the kernels that copy with tensor maps:
+// the driver's encoder, the SM count and the shared-memory limit of a kernel.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+#include <stdint.h>
+
+#include <atomic>
+#include <mutex>
+
+namespace pa {
+
+constexpr int kMaxDevices = 64;
+
+// Streaming multiprocessors of the current device (queried once per device).
+inline int sm_count()
+{
+    static std::atomic<int> cached[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 148;
+    if (dev < kMaxDevices) {
+        const int c = cached[dev].load(std::memory_order_relaxed);
+        if (c > 0) return c;
+    }
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+        n = 148;
+    if (dev < kMaxDevices) cached[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <typename Kernel>
+inline bool ensure_smem_attr(Kernel kernel, int bytes, std::atomic<uint64_t>& done_mask)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
+    if (bit && (done_mask.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return false;
+    done_mask.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
+// cuTensorMapEncodeTiled from the driver, looked up once through the runtime
+// (no link-time dependency on libcuda).
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// A row-major 16-bit matrix [rows][columns] (or, with depth > 1, `depth` of
+// them) whose boxes are 64 columns x box_rows rows, stored with the 128-byte
+// swizzle; columns a multiple of 8, strides of 16 bytes.  What lies outside
+// reads as zero.
+inline bool encode_rows_map(CUtensorMap* map, const void* base, uint64_t columns, uint64_t rows,
+                            uint64_t depth, uint64_t row_bytes, uint64_t depth_bytes,
+                            uint32_t box_rows)
+{
+    auto enc = tensor_map_encoder();
+    if (enc == nullptr) return false;
+    const cuuint64_t dims[3] = {columns, rows, depth};
+    const cuuint64_t strides[2] = {row_bytes, depth_bytes};
+    const cuuint32_t box[3] = {64u, box_rows, 1u};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace pa

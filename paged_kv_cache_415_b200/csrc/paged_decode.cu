@@ -22,13 +22,13 @@
 #include <stdint.h>
 
 #include <atomic>
-#include <mutex>
 #include <type_traits>
 
 #include "pa.h"
 #include "pa_common.cuh"
 #include "pa_host.h"
 #include "pa_selftest.h"
+#include "pa_tensor_map.h"
 #include "decode_common.cuh"
 #include "paged_decode_fp32.cuh"
 #include "paged_decode_mma.cuh"
@@ -66,54 +66,6 @@ struct DecodeArgs {
     float* k_scales = nullptr;         // row-scale pools of quantised K/V, or null (pool scales)
     float* v_scales = nullptr;
 };
-
-constexpr int kMaxDevices = 64;
-
-// Streaming multiprocessors of the current device (queried once per device).
-static int sm_count()
-{
-    static std::atomic<int> cached[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 148;
-    if (dev < kMaxDevices) {
-        const int c = cached[dev].load(std::memory_order_relaxed);
-        if (c > 0) return c;
-    }
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-        n = 148;
-    if (dev < kMaxDevices) cached[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
-template <typename Kernel>
-static bool ensure_smem_attr(Kernel kernel, int bytes, std::atomic<uint64_t>& done_mask)
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
-    if (bit && (done_mask.load(std::memory_order_relaxed) & bit)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-        return false;
-    done_mask.fetch_or(bit, std::memory_order_relaxed);
-    return true;
-}
-
-// cuTensorMapEncodeTiled from the driver, looked up once through the runtime
-// (no link-time dependency on libcuda).
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
 
 // A pool [num_blocks][B][Hkv][D] of 16-bit elements as a 4-D tensor
 // (innermost first: D, Hkv, B, num_blocks) whose box is one block of one kv
