@@ -46,19 +46,19 @@ static size_t latent_partial_rows(const LatentSplit& s, int32_t num_heads)
     return static_cast<size_t>(s.ctas) * 2 * num_heads;
 }
 
-template <typename T, int L>
-static pa_status launch_latent_decode(const LatentDecodeArgs& a, const LatentSplit& sp,
+template <typename T, int L, int N>
+static pa_status launch_latent_heads(const LatentDecodeArgs& a, const LatentSplit& sp,
                                       const void* query, const void* cache, cudaStream_t stream)
 {
-    using S = LatentDecodeShape<L>;
+    using S = LatentDecodeShape<L, N>;
     static std::atomic<uint64_t> attr_done{0};
-    auto kernel = latent_decode_kernel<T, L>;
+    auto kernel = latent_decode_kernel<T, L, N>;
     if (!ensure_smem_attr(kernel, S::kSmem, attr_done)) return PA_ERR_CUDA;
     constexpr uint64_t kRowBytes = (L + 64) * 2;
     CUtensorMap tm_query, tm_cache;
     const uint64_t rows = static_cast<uint64_t>(a.num_seqs) * a.num_heads;
     if (!encode_rows_map(&tm_query, query, L + 64, rows, 1, kRowBytes, kRowBytes * rows,
-                         (sp.group_heads + 7) / 8 * 8) ||
+                         N) ||
         !encode_rows_map(&tm_cache, cache, L + 64, a.block_size, a.num_blocks, kRowBytes,
                          kRowBytes * a.block_size, a.block_size))
         return PA_ERR_CUDA;
@@ -75,6 +75,19 @@ static pa_status launch_latent_decode(const LatentDecodeArgs& a, const LatentSpl
     return launch_overlapped(latent_combine_kernel<T, L, 1>,
                              dim3(static_cast<unsigned>((rows + kCombineWarps - 1) / kCombineWarps)),
                              dim3(kCombineWarps * 32), 0, stream, a);
+}
+
+// Columns for the heads of a group, rounded up to what a product takes.
+template <typename T, int L>
+static pa_status launch_latent_decode(const LatentDecodeArgs& a, const LatentSplit& sp,
+                                      const void* query, const void* cache, cudaStream_t stream)
+{
+    switch ((sp.group_heads + 15) / 16) {
+    case 1: return launch_latent_heads<T, L, 16>(a, sp, query, cache, stream);
+    case 2: return launch_latent_heads<T, L, 32>(a, sp, query, cache, stream);
+    case 3: return launch_latent_heads<T, L, 48>(a, sp, query, cache, stream);
+    default: return launch_latent_heads<T, L, 64>(a, sp, query, cache, stream);
+    }
 }
 
 }  // namespace pa

@@ -5,21 +5,28 @@
 // h with queries q_h:  x_ht = scale q_h . r_t,  o_h = softmax(x_h) C.  All
 // heads share the rows, so a row is read once for up to 64 heads and serves
 // both products from the same place in shared memory:
-//   S [64 heads x 64 tokens] = Q R^T       rows as the K-major operand
-//   O^T [L x heads] += C^T P^T             rows as the MN-major operand
-// Heads run along the columns of O^T, so few heads waste no tensor time:
-// the 128 lanes of each accumulator are latent elements.
+//   S^T [64 tokens x heads] = R Q^T      rows as the K-major operand
+//   O^T [L x heads] += C^T P^T           rows as the MN-major operand
+// Tokens and latent elements take the rows of the products, heads their
+// columns, so no product is wider than the heads need: with the heads in the
+// rows of S (64 at least) a batch of 16 heads drew the power of eight times
+// its products and the SM clock fell from 1.97 to 1.69 GHz.
 //
 // Work split: the 64-token tiles of all sequences form one list, cut into
-// equal runs, one a CTA (one CTA an SM: two stages of 72 KB and the query
-// fill its shared memory).  A run that cuts a sequence leaves unnormalised
-// partial sums; latent_combine_kernel adds them up in tile order, so results
-// depend on the batch's lengths and the SM count only.
+// equal runs, one a CTA (one CTA an SM: two stages of 72 KB fill its shared
+// memory).  A run that cuts a sequence leaves unnormalised partial sums;
+// latent_combine_kernel adds them up in tile order, so results depend on the
+// batch's lengths and the SM count only.
 //
 // Warps: 0-3 softmax and epilogue, 4 copies (TMA, one box of a block and 64
-// columns each), 5 products.  The softmax keeps a reference m a head; O^T is
-// rescaled only when a maximum passes m by more than 2^8, so p <= 2^8 (exact
-// in 16 bits up to the rounding every p has).
+// columns each), 5 the products for S, 6 those for O^T (apart, so that neither
+// waits in line behind the other).  A stage is filled in parts of 128 columns
+// and S starts with the first that has arrived.
+//
+// Softmax: a thread has two tokens of N / 4 heads.  It keeps a reference m a
+// head and takes p = 2^(x - m) at once; only if some x passes m by more than 8
+// (or m is not set yet) do the warps put their maxima together, move m and
+// rescale O^T.  So p <= 2^8, exact in 16 bits up to the rounding every p has.
 #pragma once
 
 #include <cuda.h>
@@ -32,8 +39,9 @@
 namespace pa {
 
 constexpr int kTile = 64;                       // tokens of a tile
-constexpr int kLatentThreads = 192;
+constexpr int kLatentThreads = 224;
 constexpr int kMaxGroupHeads = 64;              // heads a CTA serves
+constexpr int kAhead = 3;                       // tiles whose pages are looked up ahead
 constexpr float kRescaleAbove = 8.0f;           // log2 of how far p may pass 1
 
 struct LatentDecodeArgs {
@@ -61,15 +69,24 @@ __device__ __forceinline__ int32_t checked_context(const int32_t* lens, int s, i
                : -1;
 }
 
-template <int L>
+// N: columns for heads (a multiple of 16, at most 64).
+template <int L, int N>
 struct LatentDecodeShape {
     static constexpr int kChunks = L / 64 + 1;                 // 64-column chunks of a row
+    static constexpr int kParts = L / 128 + 1;                 // of a stage: the last is the rotated chunk
     static constexpr int kStageBytes = kChunks * kTile * 128;
-    static constexpr int kStages = L == 512 ? 2 : 4;
-    static constexpr int kQueryBytes = kChunks * kMaxGroupHeads * 128;
-    static constexpr int kWeightBytes = kMaxGroupHeads * 128;  // P: heads x 64 tokens
-    static constexpr int kSmem = 1024 + kQueryBytes + kStages * kStageBytes + kWeightBytes + 1024;
-    static constexpr int kOCol = 128;                          // TMEM: S 2 x 64, then O^T
+    static constexpr int kQueryChunk = N * 128;
+    static constexpr int kQueryBytes = kChunks * kQueryChunk;
+    // P^T [heads][64 tokens]; the epilogue stages 1 KB a warp in it
+    static constexpr int kWeightBytes = N * 128 > 4096 ? N * 128 : 4096;
+    static constexpr int kFixed = 1024 + kQueryBytes + kWeightBytes + 2048;
+    static constexpr int kStages = (227 * 1024 - kFixed) / kStageBytes < 5
+                                       ? (227 * 1024 - kFixed) / kStageBytes : 5;
+    static constexpr int kSmem = kFixed + kStages * kStageBytes;
+    // TMEM columns: S^T (two buffers), O^T (L / 128 blocks of 128 lanes)
+    static constexpr int kOCol = 2 * N;
+    static constexpr int kColumns = (2 + L / 128) * N;
+    static constexpr int kAlloc = kColumns <= 64 ? 64 : kColumns <= 128 ? 128 : kColumns <= 256 ? 256 : 512;
 };
 
 // The CTA's tiles, in order: tile `tile` of sequence s with context ctx.
@@ -80,8 +97,9 @@ struct TileWalk {
 
     __device__ __forceinline__ void load()
     {
-        ctx = checked_context(a->context_lens, s, a->max_context_len, a->max_blocks_per_seq,
-                              a->block_size);
+        // from one lane: what the loops count is then in uniform registers
+        ctx = __shfl_sync(kFullMask, checked_context(a->context_lens, s, a->max_context_len,
+                                                     a->max_blocks_per_seq, a->block_size), 0);
         tiles = ctx > 0 ? (ctx + kTile - 1) / kTile : 0;
     }
     __device__ __forceinline__ void start(const LatentDecodeArgs& args, int32_t s0, int32_t t0,
@@ -106,15 +124,16 @@ struct TileWalk {
     }
 };
 
-template <typename T, int L>
+template <typename T, int L, int N>
 __global__ void __launch_bounds__(kLatentThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap tm_query,
                          const __grid_constant__ CUtensorMap tm_cache,
                          const __grid_constant__ LatentDecodeArgs a)
 {
-    using S = LatentDecodeShape<L>;
+    using S = LatentDecodeShape<L, N>;
     constexpr int CH = S::kChunks;
     constexpr int ST = S::kStages;
+    constexpr int PT = S::kParts;
     constexpr int NB = L / 128;            // 128-lane blocks of O^T
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -131,21 +150,19 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     uint64_t* o_empty = bars + 4;
     uint64_t* s_full = bars + 5;           // [2]
     uint64_t* s_empty = bars + 7;          // [2]
-    uint64_t* k_full = bars + 9;           // [ST]
-    uint64_t* k_empty = bars + 9 + ST;     // [ST]
-    uint64_t* masks = bars + 9 + 2 * ST;   // [ST]: which tokens of the tile count
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 9 + 3 * ST);
+    uint64_t* masks = bars + 9;            // [ST]: which tokens of the tile count
+    uint64_t* k_empty = masks + ST;        // [ST]
+    uint64_t* k_full = k_empty + ST;       // [ST][PT]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + ST * PT);
     int32_t* run = reinterpret_cast<int32_t*>(tmem_slot + 1);     // s0, t0, count
-    int32_t* scan = run + 3;                                      // [6] warp totals
-    float* factors = reinterpret_cast<float*>(s_misc + 256);      // [64]
-    float* inv_l = factors + kMaxGroupHeads;                      // [64]
+    int32_t* scan = run + 3;                                      // [7] warp totals
+    float* factors = reinterpret_cast<float*>(s_misc + 512);      // [64]
+    float* tops = factors + kMaxGroupHeads;                       // [4][64]: of a warp's tokens
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int group = blockIdx.x;
     const int h0 = group * a.group_heads;
     const int heads = min(a.group_heads, a.num_heads - h0);
-    const int n_cols = (heads + 15) / 16 * 16;                    // columns of O^T
-    const int q_rows = (a.group_heads + 7) / 8 * 8;               // rows of a query chunk and box
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -158,12 +175,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             mbar_init(s_empty + i, 128);
         }
         for (int i = 0; i < ST; ++i) {
-            mbar_init(k_full + i, 1);
+            for (int p = 0; p < PT; ++p) mbar_init(k_full + i * PT + p, 1);
             mbar_init(k_empty + i, 1);
         }
         fence_barrier_init();
     }
-    if (warp == 5) tmem_alloc(tmem_slot, 512);
+    if (warp == 5) tmem_alloc(tmem_slot, S::kAlloc);
     grid_dependency_wait();
     allow_dependents();
 
@@ -223,147 +240,204 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         }
         __syncthreads();
     }
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
     TileWalk w;
-    w.start(a, run[0], run[1], run[2]);
+    w.start(a, __shfl_sync(kFullMask, run[0], 0), __shfl_sync(kFullMask, run[1], 0),
+            __shfl_sync(kFullMask, run[2], 0));
+    const uint32_t leader = elect_lane() ? 1u : 0u;
     bool ok = true;
 
     if (warp == 4) {
-        // Copies.  Lane l holds the page of the tile's block l.
-        const int per_tile = kTile / a.block_size;
+        // Copies.  Lane l looks up the page of a tile's block l, kAhead tiles in
+        // front of the one being copied, so that no copy waits for its table.
+        const int block_bytes = a.block_size * 128;       // of one chunk
+        int32_t parts = 0;                                // copied so far
         int32_t it = 0, seg = 0;
         bool fresh = true;                                // first tile of a segment
-        while (w.left > 0 && ok) {
-            const int st = it % ST;
-            const int32_t t0 = w.tile * kTile;
-            const int32_t valid = min(kTile, w.ctx - t0);
+        int32_t page[kAhead + 1];
+        uint64_t mask[kAhead + 1];
+        TileWalk ahead = w;
+        auto look = [&](int32_t& pg, uint64_t& mk) {
+            const int32_t t0 = ahead.tile * kTile;
+            const int32_t valid = min(kTile, ahead.ctx - t0);
             const int blocks = (valid + a.block_size - 1) / a.block_size;
-            int32_t page = 0;
+            pg = 0;
             bool bad = false;
             if (lane < blocks) {
-                page = a.block_tables[static_cast<int64_t>(w.s) * a.max_blocks_per_seq +
-                                      t0 / a.block_size + lane];
-                bad = page < 0 || page >= a.num_blocks;
+                pg = a.block_tables[static_cast<int64_t>(ahead.s) * a.max_blocks_per_seq +
+                                    t0 / a.block_size + lane];
+                bad = pg < 0 || pg >= a.num_blocks;
                 // a block outside the pool reads as zeros, beyond the map's end
-                if (bad) page = static_cast<int32_t>(a.num_blocks);
+                if (bad) pg = static_cast<int32_t>(a.num_blocks);
             }
-            uint64_t mask = valid == 64 ? ~0ull : (1ull << valid) - 1;
+            mk = valid == 64 ? ~0ull : (1ull << valid) - 1;
             const uint32_t bad_blocks = __ballot_sync(kFullMask, bad);
             if (bad_blocks != 0) {
                 if (lane == 0 && group == 0) status_or(a.d_status, PA_STATUS_BAD_BLOCK);
                 for (int b = 0; b < blocks; ++b)
                     if (bad_blocks >> b & 1)
-                        mask &= ~((a.block_size == 64 ? ~0ull : (1ull << a.block_size) - 1)
-                                  << (b * a.block_size));
+                        mk &= ~((a.block_size == 64 ? ~0ull : (1ull << a.block_size) - 1)
+                                << (b * a.block_size));
             }
-            if (it >= ST) ok = mbar_wait_warp(k_empty + st, (it / ST - 1) & 1);
-            if (!ok) break;
-            if (lane == 0) {
-                masks[st] = mask;
-                mbar_arrive_expect_tx(k_full + st, blocks * a.block_size * 128 * CH);
-            }
-            __syncwarp();
+            ahead.next();
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (ahead.left > 0) look(page[i], mask[i]);
+        while (w.left > 0 && ok) {
+            const int st = it % ST;
+            const int32_t valid = min(kTile, w.ctx - w.tile * kTile);
+            const int blocks = (valid + a.block_size - 1) / a.block_size;
+            int32_t pages[8];
+#pragma unroll
+            for (int b = 0; b < 8; ++b) pages[b] = __shfl_sync(kFullMask, page[0], b);
             uint8_t* stage = s_rows + st * S::kStageBytes;
-            for (int i0 = 0; i0 < per_tile * CH; i0 += 32) {
-                const int i = i0 + lane;
-                const int b = i % per_tile, c = i / per_tile;
-                const int32_t pg = __shfl_sync(kFullMask, page, b);
-                if (c < CH && b < blocks)
-                    tma_load_3d(stage + c * kTile * 128 + b * a.block_size * 128, &tm_cache, c * 64,
-                                0, pg, k_full + st);
+            // the rotated chunk first: it is free as soon as S is done
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                const int p = i == 0 ? PT - 1 : i - 1;
+                const int n = i == 0 ? 1 : 2;                     // chunks
+                uint64_t* bar = k_full + st * PT + p;
+                if (i == 0 && it >= ST) ok = mbar_poll_warp(k_empty + st, (it / ST - 1) & 1);
+                if (!ok) break;
+                ++parts;
+                if (leader) {
+                    // the mask is written before this arrival, its readers wait for it
+                    if (i == 0) masks[st] = mask[0];
+                    mbar_arrive_expect_tx(bar, blocks * block_bytes * n);
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) {
+                        if (b >= blocks) break;
+#pragma unroll
+                        for (int c = 2 * p; c < 2 * p + n; ++c)
+                            tma_load_3d(stage + c * kTile * 128 + b * block_bytes, &tm_cache, c * 64, 0,
+                                        pages[b], bar);
+                    }
+                }
             }
+            if (!ok) break;
             ++it;
             if (fresh) {
-                if (seg > 0) ok = mbar_wait_warp(q_empty, (seg - 1) & 1);
+                if (seg > 0) ok = mbar_poll_warp(q_empty, (seg - 1) & 1);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(q_full, CH * q_rows * 128);
-                __syncwarp();
-                if (lane < CH)
-                    tma_load_3d(s_query + lane * q_rows * 128, &tm_query, lane * 64,
-                                w.s * a.num_heads + h0, 0, q_full);
+                if (leader) {
+                    mbar_arrive_expect_tx(q_full, S::kQueryBytes);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        tma_load_3d(s_query + c * S::kQueryChunk, &tm_query, c * 64,
+                                    w.s * a.num_heads + h0, 0, q_full);
+                }
                 ++seg;
+            }
+            if (ahead.left > 0) look(page[kAhead], mask[kAhead]);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                page[i] = page[i + 1];
+                mask[i] = mask[i + 1];
             }
             fresh = w.last();
             w.next();
         }
         if (!ok) {                                        // let the copies in flight land
             if (lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
-            for (int k = max(0, it - ST); k < it; ++k) mbar_wait_warp(k_full + k % ST, (k / ST) & 1);
-            if (seg > 0) mbar_wait_warp(q_full, (seg - 1) & 1);
+            for (int k = max(0, parts - ST * PT); k < parts; ++k)
+                mbar_poll_warp(k_full + k / PT % ST * PT + (k % PT + PT - 1) % PT, (k / PT / ST) & 1);
+            if (seg > 0) mbar_poll_warp(q_full, (seg - 1) & 1);
         }
     } else if (warp == 5) {
-        // Products, one thread.  S of the next tile goes ahead of O^T of this one.
-        if (lane == 0) {
-            const uint32_t idesc_s = mma_desc<T>(64, kTile);
-            const uint32_t idesc_o = mma_desc<T>(128, n_cols, true, false);
-            const uint32_t q_addr = smem_u32(s_query), r_addr = smem_u32(s_rows), p_addr = smem_u32(s_p);
-            TileWalk nx = w;
-            int32_t nseg = 0, seg = 0;
-            bool nfresh = true, fresh = true;
-            auto scores = [&](int32_t it) {
-                const int st = it % ST, b = it & 1;
-                if (nfresh && !mbar_wait_bounded(q_full, nseg & 1)) return false;
-                if (!mbar_wait_bounded(k_full + st, (it / ST) & 1)) return false;
-                if (it >= 2 && !mbar_wait_bounded(s_empty + b, (it / 2 - 1) & 1)) return false;
-                tmem_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < CH; ++c) {
-                    const uint64_t da = desc_k_major(q_addr + c * q_rows * 128);
-                    const uint64_t db = desc_k_major(r_addr + st * S::kStageBytes + c * kTile * 128);
+        // S^T = R Q^T
+        const uint32_t idesc = mma_desc<T>(64, N);
+        const uint32_t q_addr = smem_u32(s_query), r_addr = smem_u32(s_rows);
+        int32_t it = 0, seg = 0;
+        bool fresh = true;
+        while (w.left > 0) {
+            const int st = it % ST, b = it & 1;
+            ok = (!fresh || mbar_poll_warp(q_full, seg & 1)) &&
+                 (it < 2 || mbar_poll_warp(s_empty + b, (it / 2 - 1) & 1));
+            if (!ok) break;
+            tmem_fence_after();
+            const uint32_t rows = r_addr + st * S::kStageBytes;
+            bool ready = mbar_poll_warp(k_full + st * PT + PT - 1, (it / ST) & 1);
+            ok = ready;
+#pragma unroll
+            for (int i = 0; i < PT; ++i) {
+                const int p = i == 0 ? PT - 1 : i - 1;
+                const int n = i == 0 ? 1 : 2;
+                if (!ready) ok = ok && mbar_poll_warp(k_full + st * PT + p, (it / ST) & 1);
+                // look for the next part while this one's products go out
+                if (i + 1 < PT) ready = mbar_try_wait(k_full + st * PT + i, (it / ST) & 1);
+#pragma unroll
+                for (int c = 2 * p; c < 2 * p + n; ++c) {
+                    const uint64_t da = desc_k_major(rows + c * kTile * 128);
+                    const uint64_t db = desc_k_major(q_addr + c * S::kQueryChunk);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ss(tmem + b * kTile, da + 2 * k, db + 2 * k, idesc_s, c + k > 0);
+                        mma_ss(tmem + b * N, da + 2 * k, db + 2 * k, idesc, i + k > 0 || c > 2 * p,
+                               leader);
                 }
+                ready = __all_sync(kFullMask, ready);
+            }
+            if (!ok) break;
+            fresh = w.last();
+            if (leader) {
                 mma_commit(s_full + b);
-                nfresh = nx.last();
-                if (nfresh) {
-                    mma_commit(q_empty);
-                    ++nseg;
-                }
-                nx.next();
-                return true;
-            };
-            int32_t it = 0;
-            if (w.left > 0) ok = scores(0);
-            while (w.left > 0 && ok) {
-                if (nx.left > 0) ok = scores(it + 1);
-                if (!ok) break;
-                const int st = it % ST;
-                ok = mbar_wait_bounded(p_full, it & 1) &&
-                     (!(fresh && seg > 0) || mbar_wait_bounded(o_empty, (seg - 1) & 1));
-                if (!ok) break;
-                tmem_fence_after();
-#pragma unroll 1
-                for (int b = 0; b < NB; ++b) {
-                    const uint64_t da = desc_mn_major(
-                        r_addr + st * S::kStageBytes + 2 * b * kTile * 128, kTile * 128);
-                    const uint64_t db = desc_k_major(p_addr);
+                if (fresh) mma_commit(q_empty);
+            }
+            if (fresh) ++seg;
+            ++it;
+            w.next();
+        }
+        if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
+    } else if (warp == 6) {
+        // O^T += C^T P^T
+        const uint32_t idesc = mma_desc<T>(128, N, true, false);
+        const uint32_t r_addr = smem_u32(s_rows);
+        const uint64_t db = desc_k_major(smem_u32(s_p));
+        int32_t it = 0, seg = 0;
+        bool fresh = true;
+        while (w.left > 0) {
+            const int st = it % ST;
+            ok = mbar_poll_warp(p_full, it & 1) &&
+                 (!(fresh && seg > 0) || mbar_poll_warp(o_empty, (seg - 1) & 1));
+            if (!ok) break;
+            tmem_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(tmem + S::kOCol + b * n_cols, da + k * (2048 >> 4), db + 2 * k,
-                               idesc_o, !fresh || k > 0);
-                }
+            for (int b = 0; b < NB; ++b) {
+                const uint64_t da = desc_mn_major(
+                    r_addr + st * S::kStageBytes + 2 * b * kTile * 128, kTile * 128);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ss(tmem + S::kOCol + b * N, da + k * (2048 >> 4), db + 2 * k, idesc,
+                           !fresh || k > 0, leader);
+            }
+            if (leader) {
                 mma_commit(k_empty + st);
                 mma_commit(pv_done);
-                fresh = w.last();
-                if (fresh) ++seg;
-                ++it;
-                w.next();
             }
-            if (!ok) status_or(a.d_status, PA_STATUS_TIMEOUT);
+            fresh = w.last();
+            if (fresh) ++seg;
+            ++it;
+            w.next();
         }
+        if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
     } else {
         // A wait that gave up is not repeated: the warps walk on together, so
         // that none is left alone at a barrier, and what they store is not
         // specified (PA_STATUS_TIMEOUT).
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (ok) ok = mbar_wait_warp(bar, parity);
+            if (ok) ok = mbar_poll_warp(bar, parity);
         };
-        // Softmax and epilogue.  Head r of the group is lane 32 (r / 16) + r % 16
-        // of S (rows of a 64-row product use 16 lanes of each warp's 32).
-        const int head = warp * 16 + lane;                // of the group, lanes 0-15
-        const bool mine = lane < 16 && head < heads;
+        // Softmax and epilogue.  Rows of a 64-row product use 16 lanes of each
+        // warp's 32: the warp has tokens 16 warp .. + 15 of the tile, a lane
+        // those at lane / 4 and 8 further, of heads 8 j + 2 (lane % 4) and the
+        // next:  x[4 j + 2 (token / 8) + head % 2],  m and l [2 j + head % 2].
+        constexpr int J = N / 8;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const int tok = warp * 16 + (lane >> 2);
+        const int head0 = 2 * (lane & 3);
+        // stmatrix: lane l gives head l % 8 of matrix l / 8 = (token half, j)
+        const uint32_t p_addr = smem_u32(s_p) + (lane >> 4) * 1024 + (lane & 7) * 128 +
+                                (((warp * 2 + (lane >> 3 & 1)) ^ (lane & 7)) << 4);
         // empty and bad contexts: zero rows
         for (int s = blockIdx.y; s < a.num_seqs; s += gridDim.y) {
             const int32_t c = checked_context(a.context_lens, s, a.max_context_len,
@@ -374,67 +448,109 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                                                   (static_cast<int64_t>(s) * a.num_heads + h0) * L);
             for (int i = threadIdx.x; i < heads * L / 8; i += 128) dst[i] = make_uint4(0, 0, 0, 0);
         }
-        float m = -INFINITY, l = 0.f;
+        float m[2 * J], l[2 * J];
         int32_t it = 0;
         bool fresh = true;
         bool first_seg = true;
         bool cut = w.tile > 0;                            // the segment began in another run
         while (w.left > 0) {
             const int st = it % ST, b = it & 1;
-            wait(k_full + st, (it / ST) & 1);
-            wait(s_full + b, (it / 2) & 1);
-            tmem_fence_after();
+            wait(k_full + st * PT + PT - 1, (it / ST) & 1);
             const uint64_t mask = masks[st];
             const bool whole = mask == ~0ull;
-            uint32_t x[kTile];
-            if (warp * 16 < heads) {
-                tmem_ld32(*reinterpret_cast<uint32_t(*)[32]>(x), lanes + b * kTile);
-                tmem_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + 32), lanes + b * kTile + 32);
-                tmem_wait_ld();
-            }
-            tmem_fence_before();
-            mbar_arrive(s_empty + b);
-            float top = -INFINITY;
-            if (mine) {
+            if (fresh) {
+                // columns past the heads: p = 0, and their reference never moves
 #pragma unroll
-                for (int i = 0; i < kTile; ++i) {
-                    float v = __uint_as_float(x[i]) * a.scale_log2;
-                    if (!whole && !(mask >> i & 1)) v = -INFINITY;
-                    x[i] = __float_as_uint(v);
-                    top = fmaxf(top, v);
+                for (int i = 0; i < 2 * J; ++i) {
+                    m[i] = 8 * (i >> 1) + head0 + (i & 1) < heads ? -INFINITY : INFINITY;
+                    l[i] = 0.f;
                 }
             }
-            // The reference moves when it is unset or passed by 2^8.
-            const bool moves = mine && top > m + kRescaleAbove;
-            float f = 1.f;
-            if (fresh) {
-                m = top;
-                l = 0.f;
-            } else if (moves) {
-                f = exp2_fast(m - top);
-                m = top;
-                l *= f;
+            wait(s_full + b, (it / 2) & 1);
+            tmem_fence_after();
+            uint32_t x[4 * J];
+            tmem_ld_heads<N>(x, lanes + b * N);
+            tmem_wait_ld();
+            tmem_fence_before();
+            mbar_arrive(s_empty + b);
+            const bool on[2] = {(mask >> tok & 1) != 0, (mask >> (tok + 8) & 1) != 0};
+            float y[4 * J];
+            auto shift = [&]() {                          // y = log2 of the weights
+#pragma unroll
+                for (int i = 0; i < 4 * J; ++i) {
+                    y[i] = fmaf(__uint_as_float(x[i]), a.scale_log2, -m[2 * (i >> 2) + (i & 1)]);
+                    if (!whole && !on[i >> 1 & 1]) y[i] = -INFINITY;
+                }
+            };
+            shift();
+            float high[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 4 * J; ++i) high[i & 1] = fmaxf(high[i & 1], y[i]);
+            const bool move = named_barrier_or(1, 128, fmaxf(high[0], high[1]) > kRescaleAbove);
+            if (move) {
+                // Maxima of the tile: over the lane's tokens, the warp's, the warps'.
+#pragma unroll
+                for (int i = 0; i < 2 * J; ++i) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        if (on[t])
+                            top = fmaxf(top, __uint_as_float(x[4 * (i >> 1) + 2 * t + (i & 1)]) *
+                                                 a.scale_log2);
+#pragma unroll
+                    for (int k = 4; k <= 16; k <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, k));
+                    if (lane < 4) tops[warp * kMaxGroupHeads + 8 * (i >> 1) + head0 + (i & 1)] = top;
+                }
+                named_barrier(1, 128);
+#pragma unroll
+                for (int i = 0; i < 2 * J; ++i) {
+                    const int head = 8 * (i >> 1) + head0 + (i & 1);
+                    float top = tops[head];
+#pragma unroll
+                    for (int q = 1; q < 4; ++q) top = fmaxf(top, tops[q * kMaxGroupHeads + head]);
+                    float f = 1.f;
+                    if (top > m[i] + kRescaleAbove) {     // (never for the columns past the heads)
+                        f = exp2_fast(m[i] - top);
+                        m[i] = top;
+                        l[i] *= f;
+                    }
+                    // every warp writes the same factors, and reads its own
+                    if (lane < 4) factors[head] = f;
+                }
+                __syncwarp();
+                if (!fresh) {
+                    wait(pv_done, (it - 1) & 1);
+                    tmem_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < NB * N; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o, lanes + S::kOCol + c);
+                        tmem_wait_ld();
+                        const float* fc = factors + c % N;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * fc[i]);
+                        tmem_st16(lanes + S::kOCol + c, o);
+                    }
+                    tmem_wait_st();
+                    tmem_fence_before();
+                }
+                shift();
             }
-            if (lane < 16 && head < kMaxGroupHeads) factors[head] = f;
-            const bool rescale = named_barrier_or(1, 128, !fresh && moves);
+            // The weights, rounded in pairs; where every score so far is masked
+            // (m not set) all of them are 0.
+            uint32_t pk[2 * J];
+#pragma unroll
+            for (int i = 0; i < 2 * J; ++i) {
+                const float p0 = exp2_fast(y[2 * i]), p1 = exp2_fast(y[2 * i + 1]);
+                l[2 * (i >> 1)] += p0;
+                l[2 * (i >> 1) + 1] += p1;
+                pk[i] = Elem<T>::from_float2(p0, p1);
+            }
             if (it > 0) {
                 wait(pv_done, (it - 1) & 1);
                 tmem_fence_after();
-            }
-            if (rescale) {
-#pragma unroll 1
-                for (int c = 0; c < NB * n_cols; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(o, lanes + S::kOCol + c);
-                    tmem_wait_ld();
-                    const float* fc = factors + c % n_cols;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[i] = __float_as_uint(__uint_as_float(o[i]) * fc[i]);
-                    tmem_st16(lanes + S::kOCol + c, o);
-                }
-                tmem_wait_st();
-                tmem_fence_before();
             }
             if (!whole) {
                 // rows that do not count are zeroed: 0 times what they hold may not be 0
@@ -446,63 +562,75 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                             make_uint4(0, 0, 0, 0);
                 }
             }
-            if (lane < 16 && warp * 16 < n_cols) {
-                const float sub = m == -INFINITY ? 0.f : m;
-                uint8_t* row = s_p + (head >> 3) * 1024 + (head & 7) * 128;
-                float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float p0 = mine ? exp2_fast(__uint_as_float(x[j * 8 + 2 * e]) - sub) : 0.f;
-                        const float p1 = mine ? exp2_fast(__uint_as_float(x[j * 8 + 2 * e + 1]) - sub) : 0.f;
-                        sum += p0 + p1;
-                        pk[e] = Elem<T>::from_float2(p0, p1);
-                    }
-                    *reinterpret_cast<uint4*>(row + ((j ^ (head & 7)) << 4)) =
-                        make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                }
-                l += sum;
-            }
+            for (int j = 0; j < J; j += 2)                // heads 8 j .. 8 j + 15, the warp's 16 tokens
+                stmatrix_x4_trans(p_addr + j * 1024, pk[2 * j], pk[2 * j + 1], pk[2 * j + 2],
+                                  pk[2 * j + 3]);
             fence_proxy_async_smem();
             mbar_arrive(p_full);
             fresh = w.last();
             if (fresh) {
                 // The segment is complete: normalise and store, or leave a partial.
                 const bool split = cut || w.tile + 1 < w.tiles;
-                if (mine) inv_l[head] = split ? 1.f : (l > 0.f ? 1.f / l : 0.f);
                 const int64_t slot = static_cast<int64_t>(blockIdx.y) * 2 + (first_seg ? 0 : 1);
-                if (split && mine) a.ws_ml[slot * a.num_heads + h0 + head] = make_float2(m, l);
+#pragma unroll
+                for (int i = 0; i < 2 * J; ++i) {
+#pragma unroll
+                    for (int k = 4; k <= 16; k <<= 1) l[i] += __shfl_xor_sync(kFullMask, l[i], k);
+                    if (lane < 4) tops[warp * kMaxGroupHeads + 8 * (i >> 1) + head0 + (i & 1)] = l[i];
+                }
                 named_barrier(1, 128);
+#pragma unroll
+                for (int i = 0; i < 2 * J; ++i) {
+                    const int head = 8 * (i >> 1) + head0 + (i & 1);
+                    float sum = tops[head];
+#pragma unroll
+                    for (int q = 1; q < 4; ++q) sum += tops[q * kMaxGroupHeads + head];
+                    if (lane < 4) {
+                        factors[head] = sum > 0.f ? 1.f / sum : 0.f;
+                        if (split && warp == 0 && head < heads)
+                            a.ws_ml[slot * a.num_heads + h0 + head] = make_float2(m[i], sum);
+                    }
+                }
+                __syncwarp();
                 wait(pv_done, it & 1);
                 tmem_fence_after();
-                const int d0 = warp * 32 + lane;
+                uint8_t* mine = s_p + warp * 1024;        // P^T has been used
 #pragma unroll 1
-                for (int c = 0; c < NB * n_cols; c += 16) {
-                    const int blk = c / n_cols, n0 = c % n_cols;
+                for (int c = 0; c < NB * N; c += 16) {
+                    const int n0 = c % N, d0 = c / N * 128 + warp * 32;
+                    if (n0 >= heads) continue;
                     uint32_t o[16];
                     tmem_ld16(o, lanes + S::kOCol + c);
                     tmem_wait_ld();
-                    const int d = blk * 128 + d0;
                     if (split) {
-                        float* dst = a.ws_o + (slot * a.num_heads + h0 + n0) * L + d;
+                        float* dst = a.ws_o + (slot * a.num_heads + h0 + n0) * L + d0 + lane;
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            if (n0 + i < heads) dst[static_cast<int64_t>(i) * L] = __uint_as_float(o[i]);
+                            if (n0 + i < heads) dst[i * L] = __uint_as_float(o[i]);
                     } else {
-                        T* dst = static_cast<T*>(a.out) +
-                                 (static_cast<int64_t>(w.s) * a.num_heads + h0 + n0) * L + d;
+                        // through shared memory: 16 heads x 32 elements, then 16 bytes a lane
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
+                            reinterpret_cast<T*>(mine)[i * 32 + lane] =
+                                T(__uint_as_float(o[i]) * factors[n0 + i]);
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int i = k * 8 + (lane >> 2);
                             if (n0 + i < heads)
-                                dst[static_cast<int64_t>(i) * L] =
-                                    T(__uint_as_float(o[i]) * inv_l[n0 + i]);
+                                *reinterpret_cast<uint4*>(
+                                    static_cast<T*>(a.out) +
+                                    (static_cast<int64_t>(w.s) * a.num_heads + h0 + n0 + i) * L + d0 +
+                                    (lane & 3) * 8) =
+                                    *reinterpret_cast<const uint4*>(mine + i * 64 + (lane & 3) * 16);
+                        }
+                        __syncwarp();
                     }
                 }
                 tmem_fence_before();
                 mbar_arrive(o_empty);
-                named_barrier(1, 128);                    // inv_l and factors are free again
+                named_barrier(1, 128);                    // the sums and the staging are free again
                 first_seg = cut = false;
             }
             ++it;
@@ -513,7 +641,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
-    if (warp == 5) tmem_dealloc(tmem, 512);
+    if (warp == 5) tmem_dealloc(tmem, S::kAlloc);
 }
 
 // Adds up the partials of the sequences that a cut of the work list split:

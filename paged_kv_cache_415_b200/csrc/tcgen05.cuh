@@ -59,27 +59,45 @@ __host__ __device__ constexpr uint32_t mma_desc(int m, int n, bool a_mn_major = 
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// D (TMEM) = A B (+ D if accumulate), both operands in shared memory; one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool accumulate)
+// True in one lane of a converged warp.  Called once; products and copies are
+// then issued by that lane inside warp-uniform loops.  Measured cycles to issue
+// one: a 64 x 64 product 34 so, 58 in a loop of lane 0 alone, 70 with an
+// election each; a copy of 8 KB 50, with an election each 255.
+__device__ __forceinline__ bool elect_lane()
 {
+    uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// D (TMEM) = A B (+ D if accumulate), both operands in shared memory.  The
+// whole warp executes it, the lane that passes `issue` does it.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool accumulate, uint32_t issue)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(issue)
         : "memory");
 }
 
 // The same with A in TMEM: lane = row, 16-bit elements in pairs along the columns.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                       bool accumulate)
+                                       bool accumulate, uint32_t issue)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(issue)
         : "memory");
 }
 
@@ -163,6 +181,55 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr)
         : "r"(addr));
 }
 
+// 16 lanes (from the warp's first), 4 N columns (N registers), over the whole
+// warp: register 4 j + i of lane l is row l / 4 + 8 (i / 2), column
+// 8 j + 2 (l % 4) + i % 2.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t (&r)[8], uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t (&r)[16], uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t (&r)[32], uint32_t addr)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+
+// N columns (16, 32, 48 or 64) of the same 16 lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ld_heads(uint32_t (&r)[N / 2], uint32_t addr)
+{
+    if constexpr (N == 48) {
+        tmem_ld_rows16(*reinterpret_cast<uint32_t(*)[16]>(&r[0]), addr);
+        tmem_ld_rows16(*reinterpret_cast<uint32_t(*)[8]>(&r[16]), addr + 32);
+    } else {
+        tmem_ld_rows16(r, addr);
+    }
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32])
 {
     asm volatile(
@@ -175,6 +242,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
+}
+
+// A warp's bounded wait (mbar_wait_warp), polling a while before the first
+// look at the clock: reading the global timer costs hundreds of cycles, and
+// these waits stand between the stages of a pipeline.
+__device__ __forceinline__ bool mbar_poll_warp(uint64_t* bar, uint32_t parity)
+{
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+        if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+    return mbar_wait_warp(bar, parity);
 }
 
 // One plain arrival on an mbarrier (release: what the thread wrote before is
@@ -203,6 +281,18 @@ __device__ __forceinline__ bool named_barrier_or(int id, int threads, bool v)
         : "r"(v ? 1u : 0u), "r"(id), "r"(threads)
         : "memory");
     return any != 0;
+}
+
+// Four 8 x 8 matrices of 16-bit elements to shared memory, transposed: lane l
+// gives the address of row l % 8 of matrix l / 8 in memory and holds, of matrix
+// i, column l / 4 of rows 2 (l % 4) and the next (r_i).
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t smem_addr, uint32_t r0, uint32_t r1,
+                                                  uint32_t r2, uint32_t r3)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     smem_addr),
+                 "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
 }
 
 // 2^x with relative error 2^-22; 0 for -inf.
