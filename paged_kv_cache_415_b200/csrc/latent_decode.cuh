@@ -124,6 +124,15 @@ struct TileWalk {
     }
 };
 
+__device__ __forceinline__ void load16(float (&f)[16], const float* src)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = reinterpret_cast<const float4*>(src)[i];
+        f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+    }
+}
+
 template <typename T, int L, int N>
 __global__ void __launch_bounds__(kLatentThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap tm_query,
@@ -473,6 +482,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             tmem_wait_ld();
             tmem_fence_before();
             mbar_arrive(s_empty + b);
+            // looked at early, used where P^T is written
+            const bool pv_ready = it == 0 || mbar_test(pv_done, (it - 1) & 1);
             const bool on[2] = {(mask >> tok & 1) != 0, (mask >> (tok + 8) & 1) != 0};
             float y[4 * J];
             auto shift = [&]() {                          // y = log2 of the weights
@@ -503,20 +514,34 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     if (lane < 4) tops[warp * kMaxGroupHeads + 8 * (i >> 1) + head0 + (i & 1)] = top;
                 }
                 named_barrier(1, 128);
+                float f[2 * J];
 #pragma unroll
-                for (int i = 0; i < 2 * J; ++i) {
-                    const int head = 8 * (i >> 1) + head0 + (i & 1);
-                    float top = tops[head];
+                for (int k = 0; k < J; ++k) {
+                    float2 top = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-                    for (int q = 1; q < 4; ++q) top = fmaxf(top, tops[q * kMaxGroupHeads + head]);
-                    float f = 1.f;
-                    if (top > m[i] + kRescaleAbove) {     // (never for the columns past the heads)
-                        f = exp2_fast(m[i] - top);
-                        m[i] = top;
-                        l[i] *= f;
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 v = *reinterpret_cast<const float2*>(
+                            tops + q * kMaxGroupHeads + 8 * k + head0);
+                        top.x = fmaxf(top.x, v.x);
+                        top.y = fmaxf(top.y, v.y);
                     }
-                    // every warp writes the same factors, and reads its own
-                    if (lane < 4) factors[head] = f;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float t = e ? top.y : top.x;
+                        f[2 * k + e] = 1.f;
+                        if (t > m[2 * k + e] + kRescaleAbove) {   // (never past the heads)
+                            f[2 * k + e] = exp2_fast(m[2 * k + e] - t);
+                            m[2 * k + e] = t;
+                            l[2 * k + e] *= f[2 * k + e];
+                        }
+                    }
+                }
+                // every warp writes the same factors, and reads its own
+                if (lane < 4) {
+#pragma unroll
+                    for (int k = 0; k < J; ++k)
+                        *reinterpret_cast<float2*>(factors + 8 * k + head0) =
+                            make_float2(f[2 * k], f[2 * k + 1]);
                 }
                 __syncwarp();
                 if (!fresh) {
@@ -527,7 +552,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                         uint32_t o[16];
                         tmem_ld16(o, lanes + S::kOCol + c);
                         tmem_wait_ld();
-                        const float* fc = factors + c % N;
+                        float fc[16];
+                        load16(fc, factors + c % N);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             o[i] = __float_as_uint(__uint_as_float(o[i]) * fc[i]);
@@ -548,10 +574,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 l[2 * (i >> 1) + 1] += p1;
                 pk[i] = Elem<T>::from_float2(p0, p1);
             }
-            if (it > 0) {
-                wait(pv_done, (it - 1) & 1);
-                tmem_fence_after();
-            }
+            if (!__all_sync(kFullMask, pv_ready)) wait(pv_done, (it - 1) & 1);
             if (!whole) {
                 // rows that do not count are zeroed: 0 times what they hold may not be 0
                 uint8_t* stage = s_rows + st * S::kStageBytes;
@@ -574,23 +597,31 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 const bool split = cut || w.tile + 1 < w.tiles;
                 const int64_t slot = static_cast<int64_t>(blockIdx.y) * 2 + (first_seg ? 0 : 1);
 #pragma unroll
-                for (int i = 0; i < 2 * J; ++i) {
+                for (int k = 4; k <= 16; k <<= 1)
 #pragma unroll
-                    for (int k = 4; k <= 16; k <<= 1) l[i] += __shfl_xor_sync(kFullMask, l[i], k);
-                    if (lane < 4) tops[warp * kMaxGroupHeads + 8 * (i >> 1) + head0 + (i & 1)] = l[i];
+                    for (int i = 0; i < 2 * J; ++i) l[i] += __shfl_xor_sync(kFullMask, l[i], k);
+                if (lane < 4) {
+#pragma unroll
+                    for (int k = 0; k < J; ++k) {
+                        const int head = 8 * k + head0;
+                        *reinterpret_cast<float2*>(tops + warp * kMaxGroupHeads + head) =
+                            make_float2(l[2 * k], l[2 * k + 1]);
+                        if (split && warp == 0) {
+                            float2* ml = a.ws_ml + slot * a.num_heads + h0 + head;
+                            if (head < heads) ml[0].x = m[2 * k];
+                            if (head + 1 < heads) ml[1].x = m[2 * k + 1];
+                        }
+                    }
                 }
                 named_barrier(1, 128);
-#pragma unroll
-                for (int i = 0; i < 2 * J; ++i) {
-                    const int head = 8 * (i >> 1) + head0 + (i & 1);
+                for (int head = lane; head < N; head += 32) {
                     float sum = tops[head];
 #pragma unroll
                     for (int q = 1; q < 4; ++q) sum += tops[q * kMaxGroupHeads + head];
-                    if (lane < 4) {
-                        factors[head] = sum > 0.f ? 1.f / sum : 0.f;
-                        if (split && warp == 0 && head < heads)
-                            a.ws_ml[slot * a.num_heads + h0 + head] = make_float2(m[i], sum);
-                    }
+                    // every warp writes the same factors, and reads its own
+                    factors[head] = sum > 0.f ? 1.f / sum : 0.f;
+                    if (split && warp == 0 && head < heads)
+                        a.ws_ml[slot * a.num_heads + h0 + head].y = sum;
                 }
                 __syncwarp();
                 wait(pv_done, it & 1);
@@ -610,20 +641,21 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                             if (n0 + i < heads) dst[i * L] = __uint_as_float(o[i]);
                     } else {
                         // through shared memory: 16 heads x 32 elements, then 16 bytes a lane
+                        float fc[16];
+                        load16(fc, factors + n0);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            reinterpret_cast<T*>(mine)[i * 32 + lane] =
-                                T(__uint_as_float(o[i]) * factors[n0 + i]);
+                            reinterpret_cast<T*>(mine)[i * 32 + lane] = T(__uint_as_float(o[i]) * fc[i]);
                         __syncwarp();
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int i = k * 8 + (lane >> 2);
+                            const uint4 v = *reinterpret_cast<const uint4*>(mine + i * 64 + (lane & 3) * 16);
                             if (n0 + i < heads)
                                 *reinterpret_cast<uint4*>(
                                     static_cast<T*>(a.out) +
                                     (static_cast<int64_t>(w.s) * a.num_heads + h0 + n0 + i) * L + d0 +
-                                    (lane & 3) * 8) =
-                                    *reinterpret_cast<const uint4*>(mine + i * 64 + (lane & 3) * 16);
+                                    (lane & 3) * 8) = v;
                         }
                         __syncwarp();
                     }

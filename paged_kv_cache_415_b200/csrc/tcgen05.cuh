@@ -244,11 +244,26 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
         : "memory");
 }
 
+// Whether the barrier's phase of this parity is complete; does not suspend.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // A warp's bounded wait (mbar_wait_warp), polling a while before the first
 // look at the clock: reading the global timer costs hundreds of cycles, and
 // these waits stand between the stages of a pipeline.
 __device__ __forceinline__ bool mbar_poll_warp(uint64_t* bar, uint32_t parity)
 {
+    if (__all_sync(kFullMask, mbar_test(bar, parity))) return true;
 #pragma unroll 1
     for (int i = 0; i < 256; ++i)
         if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
