@@ -1,140 +1,86 @@
-// latent_prefill.cu -- prompt attention over the paged latent pool with keys
-// and values expanded for each head.
+// latent_prefill.cu -- host entry points of prompt attention over the paged
+// latent pool: argument checks, the workspace and the two launches.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pa.h"
 #include "pa_common.cuh"
 #include "pa_host.h"
+#include "pa_tensor_map.h"
+#include "latent_prefill.cuh"
 
 namespace pa {
 
-constexpr int kRowWarps4 = 4;
-constexpr int kNope = 128;
-constexpr int kValue = 128;
-
-struct LatentArgs {
-    void* out;
-    const void* query;
-    const void* cache;
-    const void* w_kv;
-    const int32_t* block_tables;
-    const int32_t* query_starts;
-    const int32_t* context_lens;
-    int32_t num_seqs, num_tokens, num_heads, block_size, max_blocks_per_seq;
-    int64_t num_blocks;
-    int32_t max_query_len, max_context_len;
-    float scale_log2;
-    int32_t* d_status;
+// The workspace: K and V of every head, the rotated part, one mask bit a
+// token; a sequence's rows are whole tiles of keys.
+struct PrefillSpace {
+    int64_t rows;
+    size_t key_bytes, rot_bytes, mask_bytes;
+    size_t total() const { return 2 * key_bytes + rot_bytes + mask_bytes; }
 };
 
-__device__ __forceinline__ float lat_to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float lat_to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void lat_store(__half* p, float x) { *p = __float2half_rn(x); }
-__device__ __forceinline__ void lat_store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-
-__device__ __forceinline__ bool good_context(const LatentArgs& a, int32_t ctx)
+static PrefillSpace prefill_space(int32_t num_seqs, int32_t num_heads, int32_t max_context_len)
 {
-    return ctx >= 0 && ctx <= a.max_context_len &&
-           static_cast<int64_t>(ctx) <= static_cast<int64_t>(a.max_blocks_per_seq) * a.block_size;
+    PrefillSpace s;
+    s.rows = (static_cast<int64_t>(max_context_len > 0 ? max_context_len : 1) + kKvTile - 1) / kKvTile * kKvTile;
+    const size_t all = static_cast<size_t>(s.rows) * num_seqs;
+    s.key_bytes = all * num_heads * kNope * 2;
+    s.rot_bytes = all * kRot * 2;
+    s.mask_bytes = all / 8;
+    return s;
 }
 
-// Attention of one query (fp32 [L + 64] in shared memory) over the first
-// `seen` rows of sequence s, by the CTA's four warps, a token a warp at a
-// time; the normalised sum of the latent parts goes to `result` [L].
-template <typename T, int L>
-__device__ void attend_rows(const LatentArgs& a, int s, int32_t seen, const float* q, float* result,
-                            float* merge)
+// Heads a CTA of the expansion takes: its rows are loaded once for all of
+// them, and two accumulators overlap the stores of one head with the products
+// of the next; fewer heads where the grid would not fill the GPU.
+static int32_t expand_heads(int64_t tiles, int32_t num_heads)
 {
-    constexpr int W = L + 64;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float m = -INFINITY, l = 0.f, acc[L / 32];
-#pragma unroll
-    for (int i = 0; i < L / 32; ++i) acc[i] = 0.f;
-    for (int32_t t = warp; t < seen; t += kRowWarps4) {
-        const int32_t page = a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + t / a.block_size];
-        if (page < 0 || page >= a.num_blocks) {
-            if (lane == 0) status_or(a.d_status, PA_STATUS_BAD_BLOCK);
-            continue;
-        }
-        const T* row = static_cast<const T*>(a.cache) +
-                       (static_cast<int64_t>(page) * a.block_size + t % a.block_size) * W;
-        float x[W / 32];
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < W / 32; ++i) {
-            x[i] = lat_to_float(row[i * 32 + lane]);
-            dot = fmaf(x[i], q[i * 32 + lane], dot);
-        }
-#pragma unroll
-        for (int k = 16; k >= 1; k >>= 1) dot += __shfl_xor_sync(kFullMask, dot, k);
-        dot *= a.scale_log2;
-        const float mn = fmaxf(m, dot);
-        const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
-        const float p = exp2f(dot - mn);
-        m = mn;
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < L / 32; ++i) acc[i] = acc[i] * f + p * x[i];
-    }
-    float* mine = merge + warp * (L + 2);
-#pragma unroll
-    for (int i = 0; i < L / 32; ++i) mine[i * 32 + lane] = acc[i];
-    if (lane == 0) {
-        mine[L] = m;
-        mine[L + 1] = l;
-    }
-    __syncthreads();
-    float M = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kRowWarps4; ++w) M = fmaxf(M, merge[w * (L + 2) + L]);
-    const float msub = M == -INFINITY ? 0.f : M;
-    for (int w = 0; w < kRowWarps4; ++w)
-        sum += merge[w * (L + 2) + L + 1] * exp2f(merge[w * (L + 2) + L] - msub);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    for (int i = threadIdx.x; i < L; i += blockDim.x) {
-        float o = 0.f;
-        for (int w = 0; w < kRowWarps4; ++w)
-            o += merge[w * (L + 2) + i] * exp2f(merge[w * (L + 2) + L] - msub);
-        result[i] = o * inv;
-    }
-    __syncthreads();
+    int32_t n = 8;
+    while (n > 1 && tiles * ((num_heads + n - 1) / n) < sm_count()) n /= 2;
+    return n;
 }
 
 template <typename T, int L>
-__global__ void __launch_bounds__(128) latent_prefill_simple_kernel(const LatentArgs a)
+static pa_status launch_prefill(LatentPrefillArgs& a, const void* query, const void* w_kv,
+                                cudaStream_t stream)
 {
-    __shared__ float qin[kNope], q[L + 64], result[L], merge[kRowWarps4 * (L + 2)];
-    grid_dependency_wait();
-    const int h = blockIdx.x, s = blockIdx.z, i = blockIdx.y;
-    const int32_t first = a.query_starts[s], last = a.query_starts[s + 1];
-    if (first < 0 || last < first || last > a.num_tokens || last - first > a.max_query_len) {
-        if (threadIdx.x == 0) status_or(a.d_status, PA_STATUS_BAD_CONTEXT);
-        return;
-    }
-    if (i >= last - first) return;
-    int32_t ctx = a.context_lens[s];
-    const bool ok = good_context(a, ctx) && ctx >= last - first;
-    if (!ok && threadIdx.x == 0) status_or(a.d_status, PA_STATUS_BAD_CONTEXT);
-    const int32_t seen = ok ? ctx - (last - first) + i + 1 : 0;
-    const int64_t row = static_cast<int64_t>(first + i) * a.num_heads + h;
-    const T* w = static_cast<const T*>(a.w_kv) + static_cast<int64_t>(h) * (kNope + kValue) * L;
-    const T* qr = static_cast<const T*>(a.query) + row * (kNope + 64);
-    for (int e = threadIdx.x; e < kNope; e += blockDim.x) qin[e] = lat_to_float(qr[e]);
-    if (threadIdx.x < 64) q[L + threadIdx.x] = lat_to_float(qr[kNope + threadIdx.x]);
-    __syncthreads();
-    for (int c = threadIdx.x; c < L; c += blockDim.x) {
-        float v = 0.f;
-        for (int e = 0; e < kNope; ++e) v = fmaf(qin[e], lat_to_float(w[e * L + c]), v);
-        q[c] = v;
-    }
-    __syncthreads();
-    attend_rows<T, L>(a, s, seen, q, result, merge);
-    for (int e = threadIdx.x; e < kValue; e += blockDim.x) {
-        float v = 0.f;
-        for (int c = 0; c < L; ++c) v = fmaf(result[c], lat_to_float(w[(kNope + e) * L + c]), v);
-        lat_store(static_cast<T*>(a.out) + row * kValue + e, v);
-    }
+    using E = ExpandShape<L>;
+    using S = AttendShape;
+    static std::atomic<uint64_t> expand_done{0}, attend_done{0};
+    auto expand = latent_expand_kernel<T, L>;
+    auto attend = latent_attend_kernel<T>;
+    if (!ensure_smem_attr(expand, E::kSmem, expand_done) || !ensure_smem_attr(attend, S::kSmem, attend_done))
+        return PA_ERR_CUDA;
+    const uint64_t row_bytes = (L + kRot) * 2;
+    const uint64_t kv_rows = static_cast<uint64_t>(a.rows);
+    const uint64_t heads = static_cast<uint64_t>(a.num_heads);
+    const uint64_t w_rows = heads * (kNope + kValue);
+    const uint64_t q_bytes = (kNope + kRot) * 2;
+    const uint64_t planes = static_cast<uint64_t>(a.num_seqs) * heads;
+    CUtensorMap tm_cache, tm_w, tm_q, tm_k, tm_v, tm_r;
+    if (!encode_rows_map(&tm_cache, a.cache, L + kRot, a.block_size, a.num_blocks, row_bytes,
+                         row_bytes * a.block_size, a.block_size) ||
+        !encode_rows_map(&tm_w, w_kv, L, w_rows, 1, L * 2, L * 2 * w_rows, kNope + kValue) ||
+        !encode_rows_map(&tm_q, query, kNope + kRot, a.num_tokens, heads, q_bytes * heads, q_bytes,
+                         kQueryTile) ||
+        !encode_rows_map(&tm_k, a.ws_k, kNope, kv_rows, planes, kNope * 2, kNope * 2 * kv_rows, kKvTile) ||
+        !encode_rows_map(&tm_v, a.ws_v, kValue, kv_rows, planes, kValue * 2, kValue * 2 * kv_rows, kKvTile) ||
+        !encode_rows_map(&tm_r, a.ws_rot, kRot, kv_rows, a.num_seqs, kRot * 2, kRot * 2 * kv_rows, kKvTile))
+        return PA_ERR_CUDA;
+    const int64_t tiles = a.rows / kKvTile;
+    a.heads_per_cta = expand_heads(tiles * a.num_seqs, a.num_heads);
+    pa_status st = launch_overlapped(
+        expand,
+        dim3((a.num_heads + a.heads_per_cta - 1) / a.heads_per_cta, static_cast<unsigned>(tiles), a.num_seqs),
+        dim3(kExpandThreads), E::kSmem, stream, tm_cache, tm_w, a);
+    if (st != PA_OK) return st;
+    const int32_t pairs = (a.max_query_len + 2 * kQueryTile - 1) / (2 * kQueryTile);
+    return launch_overlapped(attend, dim3(a.num_heads, pairs, a.num_seqs), dim3(kAttendThreads), S::kSmem,
+                             stream, tm_q, tm_k, tm_v, tm_r, a);
 }
 
 }  // namespace pa
@@ -148,8 +94,7 @@ extern "C" size_t pa_latent_prefill_workspace_size(int32_t num_seqs, int32_t num
         !supported_latent(latent_dim, 64) || !supported_latent_block(block_size) ||
         num_heads > kMaxLatentHeads)
         return 0;
-    const size_t rows = (static_cast<size_t>(max_context_len) + 127) / 128 * 128 * num_seqs;
-    return rows * (static_cast<size_t>(num_heads) * (kNope + kValue) + 64) * 2;
+    return prefill_space(num_seqs, num_heads, max_context_len).total();
 }
 
 extern "C" pa_status pa_latent_prefill(
@@ -180,14 +125,22 @@ extern "C" pa_status pa_latent_prefill(
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
         return PA_ERR_INVALID_ARG;
     if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
-    LatentArgs a = {};
+    const PrefillSpace sp = prefill_space(num_seqs, num_heads, max_context_len);
+    if (sp.rows > 65535LL * kKvTile || num_blocks > 0x7fffffff ||
+        max_query_len > 65535LL * 2 * kQueryTile)
+        return PA_ERR_UNSUPPORTED;
+    LatentPrefillArgs a = {};
     a.out = out;
-    a.query = query;
     a.cache = cache;
-    a.w_kv = w_kv;
     a.block_tables = block_tables;
     a.query_starts = query_starts;
     a.context_lens = context_lens;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.ws_k = ws;
+    a.ws_v = ws + sp.key_bytes;
+    a.ws_rot = ws + 2 * sp.key_bytes;
+    a.ws_mask = reinterpret_cast<uint32_t*>(ws + 2 * sp.key_bytes + sp.rot_bytes);
+    a.rows = static_cast<int32_t>(sp.rows);
     a.num_seqs = num_seqs;
     a.num_tokens = num_tokens;
     a.num_heads = num_heads;
@@ -198,10 +151,9 @@ extern "C" pa_status pa_latent_prefill(
     a.max_context_len = max_context_len;
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     a.d_status = d_status;
-    auto kernel = dtype == PA_DTYPE_F16
-                      ? (latent_dim == 512 ? latent_prefill_simple_kernel<__half, 512>
-                                           : latent_prefill_simple_kernel<__half, 256>)
-                      : (latent_dim == 512 ? latent_prefill_simple_kernel<__nv_bfloat16, 512>
-                                           : latent_prefill_simple_kernel<__nv_bfloat16, 256>);
-    return launch_overlapped(kernel, dim3(num_heads, max_query_len, num_seqs), dim3(128), 0, stream, a);
+    if (dtype == PA_DTYPE_F16)
+        return latent_dim == 512 ? launch_prefill<__half, 512>(a, query, w_kv, stream)
+                                 : launch_prefill<__half, 256>(a, query, w_kv, stream);
+    return latent_dim == 512 ? launch_prefill<__nv_bfloat16, 512>(a, query, w_kv, stream)
+                             : launch_prefill<__nv_bfloat16, 256>(a, query, w_kv, stream);
 }

@@ -1,0 +1,568 @@
+// latent_prefill.cuh -- prompt attention over the paged latent pool with
+// keys and values expanded (sm_100a tensor cores), in two launches:
+//
+//   latent_expand_kernel   K_h = C W_h^K, V_h = C W_h^V for every token of
+//                          every context: a product of 128 tokens x 256
+//                          columns (one head's key and value) over L, rounded
+//                          once to 16 bits and kept in the workspace.  The
+//                          tokens' rows stay in shared memory while the heads'
+//                          weights stream past them.
+//   latent_attend_kernel   causal attention of 256 queries of one head:
+//                          S = Q K^T over 128 + 64 elements (the rotated part
+//                          is shared by the heads), P V over 128.
+//
+// Both are bound by the tensor cores; the expansion costs 2 L 256 operations a
+// token and head, the attention 2 (192 + 128) a query, visible token and head.
+#pragma once
+
+#include <cuda.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "pa_common.cuh"
+#include "tcgen05.cuh"
+
+namespace pa {
+
+constexpr int kNope = 128;                      // unrotated elements of a head's key
+constexpr int kValue = 128;                     // elements of a head's value
+constexpr int kRot = 64;                        // rotated elements, shared by the heads
+constexpr int kKvTile = 128;                    // tokens of a tile of keys
+constexpr int kQueryTile = 128;                 // queries of a tile; a CTA takes two
+
+struct LatentPrefillArgs {
+    void* out;
+    const void* cache;
+    const int32_t* block_tables;
+    const int32_t* query_starts;
+    const int32_t* context_lens;
+    void* ws_k;                 // [S][H][rows][128]
+    void* ws_v;                 // [S][H][rows][128]
+    void* ws_rot;               // [S][rows][64]
+    uint32_t* ws_mask;          // [S][rows / 32]: tokens that count
+    int32_t rows;               // max_context_len rounded up to whole tiles
+    int32_t num_seqs, num_tokens, num_heads, heads_per_cta, block_size, max_blocks_per_seq;
+    int64_t num_blocks;
+    int32_t max_query_len, max_context_len;
+    float scale_log2;
+    int32_t* d_status;
+};
+
+// A sequence's rows of the batch and its context.  `first` < 0: the starts are
+// bad and its rows are left alone; `context` < 0: its rows are zeroed.
+struct PromptSpan {
+    int32_t first, count, context;
+};
+
+__device__ __forceinline__ PromptSpan prompt_span(const LatentPrefillArgs& a, int s)
+{
+    PromptSpan p;
+    p.first = a.query_starts[s];
+    const int32_t end = a.query_starts[s + 1];
+    p.count = end - p.first;
+    if (p.first < 0 || end < p.first || end > a.num_tokens || p.count > a.max_query_len) {
+        p.first = -1;
+        p.count = 0;
+    }
+    p.context = a.context_lens[s];
+    if (p.context < p.count || p.context > a.max_context_len ||
+        static_cast<int64_t>(p.context) > static_cast<int64_t>(a.max_blocks_per_seq) * a.block_size)
+        p.context = -1;
+    return p;
+}
+
+// ---------------------------------------------------------------------------
+// Expansion
+// ---------------------------------------------------------------------------
+
+template <int L>
+struct ExpandShape {
+    static constexpr int kChunks = L / 64;
+    static constexpr int kRowsBytes = kChunks * kKvTile * 128;
+    static constexpr int kStageBytes = (kNope + kValue) * 128;     // 64 columns of a head's weights
+    static constexpr int kStages = 3;
+    static constexpr int kSmem = 1024 + kRowsBytes + kStages * kStageBytes + 1024;
+};
+
+constexpr int kExpandThreads = 192;
+
+// Grid (group of heads, tile of 128 tokens, sequence).  Warps: 0-3 store, 4
+// copies, 5 products; two accumulators of 256 columns alternate.
+template <typename T, int L>
+__global__ void __launch_bounds__(kExpandThreads, 1)
+    latent_expand_kernel(const __grid_constant__ CUtensorMap tm_cache,
+                         const __grid_constant__ CUtensorMap tm_weights,
+                         const __grid_constant__ LatentPrefillArgs a)
+{
+    using S = ExpandShape<L>;
+    constexpr int CH = S::kChunks;
+    constexpr int ST = S::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* s_rows = smem;
+    uint8_t* s_weights = smem + S::kRowsBytes;
+    uint64_t* r_full = reinterpret_cast<uint64_t*>(s_weights + ST * S::kStageBytes);   // [CH]
+    uint64_t* w_full = r_full + CH;        // [ST]
+    uint64_t* w_empty = w_full + ST;       // [ST]
+    uint64_t* o_full = w_empty + ST;       // [2]
+    uint64_t* o_empty = o_full + 2;        // [2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_empty + 2);
+
+    const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int s = blockIdx.z, t0 = blockIdx.y * kKvTile;
+    const int h0 = blockIdx.x * a.heads_per_cta;
+    const int heads = min(a.heads_per_cta, a.num_heads - h0);
+    grid_dependency_wait();
+    const PromptSpan span = prompt_span(a, s);
+    allow_dependents();
+    if (span.count == 0 || t0 >= span.context) return;    // (a bad context is negative)
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < CH; ++i) mbar_init(r_full + i, 1);
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(w_full + i, 1);
+            mbar_init(w_empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(o_full + i, 1);
+            mbar_init(o_empty + i, 128);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 5) tmem_alloc(tmem_slot, 512);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
+    const uint32_t leader = elect_lane() ? 1u : 0u;
+    bool ok = true;
+
+    if (warp == 4) {
+        const int valid = min(kKvTile, span.context - t0);
+        const int blocks = (valid + a.block_size - 1) / a.block_size;
+        const int block_bytes = a.block_size * 128;
+        int32_t page = 0;
+        if (lane < blocks) {
+            page = a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + t0 / a.block_size + lane];
+            // a block outside the pool reads as zeros, beyond the map's end
+            if (page < 0 || page >= a.num_blocks) {
+                page = static_cast<int32_t>(a.num_blocks);
+                if (blockIdx.x == 0) status_or(a.d_status, PA_STATUS_BAD_BLOCK);
+            }
+        }
+        int32_t it = 0;
+        for (int h = 0; h < heads && ok; ++h) {
+            for (int c = 0; c < CH && ok; ++c, ++it) {
+                const int st = it % ST;
+                if (it >= ST) ok = mbar_poll_warp(w_empty + st, (it / ST - 1) & 1);
+                if (!ok) break;
+                if (leader) {
+                    mbar_arrive_expect_tx(w_full + st, S::kStageBytes);
+                    tma_load_3d(s_weights + st * S::kStageBytes, &tm_weights, c * 64,
+                                (h0 + h) * (kNope + kValue), 0, w_full + st);
+                }
+                if (h == 0) {                             // the rows, with the first head's weights
+                    if (leader) mbar_arrive_expect_tx(r_full + c, blocks * block_bytes);
+                    for (int b = 0; b < blocks; ++b) {
+                        const int32_t pg = __shfl_sync(kFullMask, page, b);
+                        if (leader)
+                            tma_load_3d(s_rows + c * kKvTile * 128 + b * block_bytes, &tm_cache, c * 64,
+                                        0, pg, r_full + c);
+                    }
+                }
+            }
+        }
+        if (!ok) {                                        // let the copies in flight land
+            if (lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
+            for (int k = max(0, it - ST); k < it; ++k) mbar_poll_warp(w_full + k % ST, (k / ST) & 1);
+            for (int c = 0; c < min(CH, it); ++c) mbar_poll_warp(r_full + c, 0);
+        }
+    } else if (warp == 5) {
+        const uint32_t idesc = mma_desc<T>(kKvTile, kNope + kValue);
+        const uint32_t r_addr = smem_u32(s_rows), w_addr = smem_u32(s_weights);
+        int32_t it = 0;
+        for (int h = 0; h < heads && ok; ++h) {
+            const int b = h & 1;
+            if (h >= 2) ok = mbar_poll_warp(o_empty + b, (h / 2 - 1) & 1);
+            tmem_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < CH && ok; ++c, ++it) {
+                const int st = it % ST;
+                ok = mbar_poll_warp(w_full + st, (it / ST) & 1) && (h > 0 || mbar_poll_warp(r_full + c, 0));
+                if (!ok) break;
+                const uint64_t da = desc_k_major(r_addr + c * kKvTile * 128);
+                const uint64_t db = desc_k_major(w_addr + st * S::kStageBytes);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ss(tmem + b * 256, da + 2 * k, db + 2 * k, idesc, c + k > 0, leader);
+                if (leader) mma_commit(w_empty + st);
+            }
+            if (leader && ok) mma_commit(o_full + b);
+        }
+        if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
+    } else {
+        // A thread has one token's row.
+        const int r = threadIdx.x;
+        const int32_t t = t0 + r;
+        bool counts = t < span.context;
+        int32_t page = 0;
+        if (counts) {
+            page = a.block_tables[static_cast<int64_t>(s) * a.max_blocks_per_seq + t / a.block_size];
+            counts = page >= 0 && page < a.num_blocks;
+        }
+        const int64_t srow = static_cast<int64_t>(s) * a.rows + t;
+        if (blockIdx.x == 0) {
+            const uint32_t word = __ballot_sync(kFullMask, counts);
+            if (lane == 0) a.ws_mask[srow >> 5] = word;
+            // the rotated part, the same for every head
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const T*>(a.cache) +
+                (static_cast<int64_t>(page) * a.block_size + t % a.block_size) * (L + kRot) + L);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.ws_rot) + srow * kRot);
+            uint4 v[kRot / 8];
+#pragma unroll
+            for (int i = 0; i < kRot / 8; ++i) v[i] = counts ? ld_nc_v4(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kRot / 8; ++i) dst[i] = v[i];
+        }
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        for (int h = 0; h < heads; ++h) {
+            const int b = h & 1;
+            ok = mbar_poll_warp(o_full + b, (h / 2) & 1);
+            if (!ok) break;
+            tmem_fence_after();
+            const int64_t row = (static_cast<int64_t>(s) * a.num_heads + h0 + h) * a.rows + t;
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {                 // 32 columns each: four of K, four of V
+                uint32_t o[32];
+                tmem_ld32(o, lanes + b * 256 + c * 32);
+                tmem_wait_ld();
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(c < 4 ? a.ws_k : a.ws_v) +
+                                                      row * kNope + (c & 3) * 32);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        p[e] = Elem<T>::from_float2(__uint_as_float(o[8 * i + 2 * e]),
+                                                    __uint_as_float(o[8 * i + 2 * e + 1]));
+                    // a token that does not count is a row of zeros: 0 times what
+                    // its place holds may not be 0
+                    dst[i] = counts ? make_uint4(p[0], p[1], p[2], p[3]) : make_uint4(0, 0, 0, 0);
+                }
+            }
+            tmem_fence_before();
+            mbar_arrive(o_empty + b);
+        }
+        if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 5) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Attention
+// ---------------------------------------------------------------------------
+
+struct AttendShape {
+    static constexpr int kChunks = (kNope + kRot) / 64;
+    static constexpr int kQueryBytes = kChunks * kQueryTile * 128;
+    static constexpr int kKeyBytes = kChunks * kKvTile * 128;
+    static constexpr int kValueBytes = kValue / 64 * kKvTile * 128;
+    static constexpr int kKeyStages = 2;
+    static constexpr int kSmem = 1024 + 2 * kQueryBytes + kKeyStages * kKeyBytes + kValueBytes + 512;
+    // TMEM: S of the two query tiles (P takes the first half of its S), O of both
+    static constexpr int kOCol = 256;
+};
+
+constexpr int kAttendThreads = 320;
+
+// Grid (head, pair of query tiles with the longest first, sequence).  Warps:
+// 0-3 and 4-7 softmax of one query tile each, a thread a query; 8 copies; 9
+// products.  While one tile's scores go through the softmax, the products of
+// the other run.
+template <typename T>
+__global__ void __launch_bounds__(kAttendThreads, 1)
+    latent_attend_kernel(const __grid_constant__ CUtensorMap tm_query,
+                         const __grid_constant__ CUtensorMap tm_key,
+                         const __grid_constant__ CUtensorMap tm_value,
+                         const __grid_constant__ CUtensorMap tm_rot,
+                         const __grid_constant__ LatentPrefillArgs a)
+{
+    using S = AttendShape;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint8_t* s_query = smem;
+    uint8_t* s_key = s_query + 2 * S::kQueryBytes;
+    uint8_t* s_value = s_key + S::kKeyStages * S::kKeyBytes;
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(s_value + S::kValueBytes);    // [2]
+    uint64_t* k_full = q_full + 2;         // [2]
+    uint64_t* k_empty = k_full + 2;        // [2]
+    uint64_t* v_full = k_empty + 2;
+    uint64_t* v_empty = v_full + 1;
+    uint64_t* s_full = v_empty + 1;        // [2]
+    uint64_t* p_full = s_full + 2;         // [2]
+    uint64_t* pv_done = p_full + 2;        // [2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pv_done + 2);
+
+    const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int h = blockIdx.x, s = blockIdx.z;
+    const int row0 = (gridDim.y - 1 - blockIdx.y) * 2 * kQueryTile;
+    grid_dependency_wait();
+    const PromptSpan span = prompt_span(a, s);
+    if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0 && (span.first < 0 || span.context < 0))
+        status_or(a.d_status, PA_STATUS_BAD_CONTEXT);
+    allow_dependents();
+    if (row0 >= span.count) return;
+    if (span.context < 0) {                               // zero rows
+        const int n = min(2 * kQueryTile, span.count - row0);
+        for (int i = threadIdx.x; i < n * (kValue / 8); i += kAttendThreads) {
+            const int64_t row = static_cast<int64_t>(span.first + row0 + i / (kValue / 8)) * a.num_heads + h;
+            reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * kValue)[i % (kValue / 8)] =
+                make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
+    // Tiles of keys each query tile sees: up to its last query's position.
+    const int32_t before = span.context - span.count;     // tokens before the first query
+    int32_t steps[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int32_t r = row0 + t * kQueryTile;
+        steps[t] = r >= span.count ? 0
+                                   : (before + min(span.count, r + kQueryTile) + kKvTile - 1) / kKvTile;
+        steps[t] = __shfl_sync(kFullMask, steps[t], 0);
+    }
+    const int32_t total = max(steps[0], steps[1]);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 1);
+            mbar_init(k_full + i, 1);
+            mbar_init(k_empty + i, 1);
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 128);
+            mbar_init(pv_done + i, 1);
+        }
+        mbar_init(v_full, 1);
+        mbar_init(v_empty, 1);
+        fence_barrier_init();
+    }
+    if (warp == 9) tmem_alloc(tmem_slot, 512);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = __shfl_sync(kFullMask, *tmem_slot, 0);
+    const uint32_t leader = elect_lane() ? 1u : 0u;
+    bool ok = true;
+
+    if (warp == 8) {
+        auto key = [&](int32_t i) {
+            const int st = i & 1;
+            if (leader) {
+                mbar_arrive_expect_tx(k_full + st, S::kKeyBytes);
+                uint8_t* dst = s_key + st * S::kKeyBytes;
+                tma_load_3d(dst, &tm_key, 0, i * kKvTile, s * a.num_heads + h, k_full + st);
+                tma_load_3d(dst + kKvTile * 128, &tm_key, 64, i * kKvTile, s * a.num_heads + h, k_full + st);
+                tma_load_3d(dst + 2 * kKvTile * 128, &tm_rot, 0, i * kKvTile, s, k_full + st);
+            }
+        };
+        int32_t keys = 0, values = 0;
+        if (leader) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (steps[t] == 0) continue;
+                mbar_arrive_expect_tx(q_full + t, S::kQueryBytes);
+#pragma unroll
+                for (int c = 0; c < S::kChunks; ++c)
+                    tma_load_3d(s_query + t * S::kQueryBytes + c * kQueryTile * 128, &tm_query, c * 64,
+                                span.first + row0 + t * kQueryTile, h, q_full + t);
+            }
+        }
+        key(keys++);
+        for (; values < total; ++values) {
+            if (values > 0) ok = mbar_poll_warp(v_empty, (values - 1) & 1);
+            if (!ok) break;
+            if (leader) {
+                mbar_arrive_expect_tx(v_full, S::kValueBytes);
+#pragma unroll
+                for (int c = 0; c < kValue / 64; ++c)
+                    tma_load_3d(s_value + c * kKvTile * 128, &tm_value, c * 64, values * kKvTile,
+                                s * a.num_heads + h, v_full);
+            }
+            if (keys < total) {
+                if (keys >= 2) ok = mbar_poll_warp(k_empty + (keys & 1), (keys / 2 - 1) & 1);
+                if (!ok) break;
+                key(keys++);
+            }
+        }
+        if (!ok) {                                        // let the copies in flight land
+            if (lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
+            for (int t = 0; t < 2; ++t)
+                if (steps[t] > 0) mbar_poll_warp(q_full + t, 0);
+            for (int k = max(0, keys - 2); k < keys; ++k) mbar_poll_warp(k_full + (k & 1), (k / 2) & 1);
+            mbar_poll_warp(v_full, (values - 1) & 1);
+        }
+    } else if (warp == 9) {
+        const uint32_t idesc_s = mma_desc<T>(kQueryTile, kKvTile);
+        const uint32_t idesc_o = mma_desc<T>(kQueryTile, kValue, false, true);
+        const uint32_t q_addr = smem_u32(s_query), k_addr = smem_u32(s_key), v_addr = smem_u32(s_value);
+        auto scores = [&](int t, int32_t i) {
+            ok = ok && mbar_poll_warp(k_full + (i & 1), (i / 2) & 1);
+            if (!ok) return;
+#pragma unroll
+            for (int c = 0; c < S::kChunks; ++c) {
+                const uint64_t da = desc_k_major(q_addr + t * S::kQueryBytes + c * kQueryTile * 128);
+                const uint64_t db = desc_k_major(k_addr + (i & 1) * S::kKeyBytes + c * kKvTile * 128);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ss(tmem + t * kKvTile, da + 2 * k, db + 2 * k, idesc_s, c + k > 0, leader);
+            }
+            if (leader) mma_commit(s_full + t);
+        };
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (steps[t] == 0) continue;
+            ok = ok && mbar_poll_warp(q_full + t, 0);
+            scores(t, 0);
+        }
+        if (leader && ok) mma_commit(k_empty);
+        for (int32_t i = 0; i < total && ok; ++i) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (i < steps[t] && ok) {
+                    ok = mbar_poll_warp(v_full, i & 1) && mbar_poll_warp(p_full + t, i & 1);
+                    if (!ok) break;
+                    tmem_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kKvTile / 16; ++k)
+                        mma_ts(tmem + S::kOCol + t * kValue, tmem + t * kKvTile + k * 8,
+                               desc_mn_major(v_addr + k * 2048, kKvTile * 128), idesc_o, i + k > 0, leader);
+                    if (leader) mma_commit(pv_done + t);
+                    // S of the next tile takes the place of P: products run in order
+                    if (i + 1 < steps[t]) scores(t, i + 1);
+                }
+            }
+            if (leader && ok) {
+                mma_commit(v_empty);
+                mma_commit(k_empty + ((i + 1) & 1));
+            }
+        }
+        if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
+    } else {
+        const int t = warp >> 2;
+        const int32_t n = steps[t];
+        const int32_t r = row0 + t * kQueryTile + (threadIdx.x & 127);          // the thread's query
+        // the last token it sees; rows past the queries see what the last one does
+        const int32_t last = before + min(r, span.count - 1);
+        const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t s_tmem = tmem + quarter + t * kKvTile;
+        const uint32_t o_tmem = tmem + quarter + S::kOCol + t * kValue;
+        float m = -INFINITY, l = 0.f;
+        for (int32_t i = 0; i < n; ++i) {
+            const int32_t t0 = i * kKvTile;
+            const uint4 word = *reinterpret_cast<const uint4*>(a.ws_mask +
+                                                               ((static_cast<int64_t>(s) * a.rows + t0) >> 5));
+            ok = mbar_poll_warp(s_full + t, i & 1);
+            if (!ok) break;
+            tmem_fence_after();
+            uint32_t x[kKvTile];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                tmem_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * c), s_tmem + 32 * c);
+            tmem_wait_ld();
+            float unit = a.scale_log2;
+            const bool whole = (word.x & word.y & word.z & word.w) == ~0u && last - t0 >= kKvTile - 1;
+            if (!__all_sync(kFullMask, whole) || unit < 0.f) {
+                // scaled here: a masked score is -inf whatever the scale
+                const uint32_t words[4] = {word.x, word.y, word.z, word.w};
+#pragma unroll
+                for (int e = 0; e < kKvTile; ++e) {
+                    const bool sees = e <= last - t0 && (words[e >> 5] >> (e & 31) & 1);
+                    x[e] = __float_as_uint(sees ? __uint_as_float(x[e]) * unit : -INFINITY);
+                }
+                unit = 1.f;
+            }
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < kKvTile; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e]));
+            const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
+            // The reference moves where it is unset or passed by 2^8.
+            const bool moves = peak > m + 8.0f;
+            if (__any_sync(kFullMask, moves)) {
+                const float f = moves ? exp2_fast(m - peak) : 1.f;
+                if (moves) m = peak;
+                l *= f;
+                if (i > 0) {
+                    ok = mbar_poll_warp(pv_done + t, (i - 1) & 1);
+                    if (!ok) break;
+                    tmem_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < kValue; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o, o_tmem + c);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(o_tmem + c, o);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            const float sub = m == -INFINITY ? 0.f : m;
+            float sum[2] = {0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t p[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float p0 = exp2_fast(fmaf(__uint_as_float(x[64 * c + 2 * e]), unit, -sub));
+                    const float p1 = exp2_fast(fmaf(__uint_as_float(x[64 * c + 2 * e + 1]), unit, -sub));
+                    sum[0] += p0;
+                    sum[1] += p1;
+                    p[e] = Elem<T>::from_float2(p0, p1);
+                }
+                tmem_st32(s_tmem + 32 * c, p);
+            }
+            l += sum[0] + sum[1];
+            tmem_wait_st();
+            tmem_fence_before();
+            mbar_arrive(p_full + t);
+        }
+        if (ok && n > 0) ok = mbar_poll_warp(pv_done + t, (n - 1) & 1);
+        if (ok && n > 0) {
+            tmem_fence_after();
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            T* dst = static_cast<T*>(a.out) +
+                     (static_cast<int64_t>(span.first + min(r, span.count - 1)) * a.num_heads + h) * kValue;
+#pragma unroll 1
+            for (int c = 0; c < kValue; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, o_tmem + c);
+                tmem_wait_ld();
+                if (r < span.count) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            p[e] = Elem<T>::from_float2(__uint_as_float(o[8 * j + 2 * e]) * inv,
+                                                        __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
+                        reinterpret_cast<uint4*>(dst + c)[j] = make_uint4(p[0], p[1], p[2], p[3]);
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
+    }
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace pa
