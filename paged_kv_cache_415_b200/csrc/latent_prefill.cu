@@ -34,14 +34,22 @@ static PrefillSpace prefill_space(int32_t num_seqs, int32_t num_heads, int32_t m
     return s;
 }
 
-// Heads a CTA of the expansion takes: its rows are loaded once for all of
-// them, and two accumulators overlap the stores of one head with the products
-// of the next; fewer heads where the grid would not fill the GPU.
+// Heads a CTA of the expansion takes.  Its rows are loaded once for all of
+// them; a wave of CTAs costs its heads and about 1.5 more of start and end, so
+// the number that makes waves x (heads + 1.5) least is taken.
 static int32_t expand_heads(int64_t tiles, int32_t num_heads)
 {
-    int32_t n = 8;
-    while (n > 1 && tiles * ((num_heads + n - 1) / n) < sm_count()) n /= 2;
-    return n;
+    int32_t best = 1;
+    double least = 0.0;
+    for (int32_t n = 1; n <= num_heads; ++n) {
+        const int64_t ctas = tiles * ((num_heads + n - 1) / n);
+        const double cost = static_cast<double>((ctas + sm_count() - 1) / sm_count()) * (n + 1.5);
+        if (n == 1 || cost < least) {
+            least = cost;
+            best = n;
+        }
+    }
+    return best;
 }
 
 template <typename T, int L>
@@ -64,7 +72,7 @@ static pa_status launch_prefill(LatentPrefillArgs& a, const void* query, const v
     CUtensorMap tm_cache, tm_w, tm_q, tm_k, tm_v, tm_r;
     if (!encode_rows_map(&tm_cache, a.cache, L + kRot, a.block_size, a.num_blocks, row_bytes,
                          row_bytes * a.block_size, a.block_size) ||
-        !encode_rows_map(&tm_w, w_kv, L, w_rows, 1, L * 2, L * 2 * w_rows, kNope + kValue) ||
+        !encode_rows_map(&tm_w, w_kv, L, w_rows, 1, L * 2, L * 2 * w_rows, 128) ||
         !encode_rows_map(&tm_q, query, kNope + kRot, a.num_tokens, heads, q_bytes * heads, q_bytes,
                          kQueryTile) ||
         !encode_rows_map(&tm_k, a.ws_k, kNope, kv_rows, planes, kNope * 2, kNope * 2 * kv_rows, kKvTile) ||
@@ -76,7 +84,8 @@ static pa_status launch_prefill(LatentPrefillArgs& a, const void* query, const v
     pa_status st = launch_overlapped(
         expand,
         dim3((a.num_heads + a.heads_per_cta - 1) / a.heads_per_cta, static_cast<unsigned>(tiles), a.num_seqs),
-        dim3(kExpandThreads), E::kSmem, stream, tm_cache, tm_w, a);
+        dim3(kExpandThreads), E::kSmem, stream, tm_cache, tm_w, tm_k, tm_v,
+        a);
     if (st != PA_OK) return st;
     const int32_t pairs = (a.max_query_len + 2 * kQueryTile - 1) / (2 * kQueryTile);
     return launch_overlapped(attend, dim3(a.num_heads, pairs, a.num_seqs), dim3(kAttendThreads), S::kSmem,

@@ -79,19 +79,25 @@ template <int L>
 struct ExpandShape {
     static constexpr int kChunks = L / 64;
     static constexpr int kRowsBytes = kChunks * kKvTile * 128;
-    static constexpr int kStageBytes = (kNope + kValue) * 128;     // 64 columns of a head's weights
-    static constexpr int kStages = 3;
-    static constexpr int kSmem = 1024 + kRowsBytes + kStages * kStageBytes + 1024;
+    static constexpr int kStageBytes = 128 * 128;   // 64 columns of a head's key or value weights
+    static constexpr int kStages = L == 512 ? 5 : 8;
+    static constexpr int kOutBytes = kKvTile * 128; // 64 columns of a result, on their way out
+    static constexpr int kSmem = 1024 + kRowsBytes + kStages * kStageBytes + kOutBytes + 512;
 };
 
 constexpr int kExpandThreads = 192;
 
 // Grid (group of heads, tile of 128 tokens, sequence).  Warps: 0-3 store, 4
-// copies, 5 products; two accumulators of 256 columns alternate.
+// copies, 5 products; two accumulators of 256 columns (key, value) alternate.
+// Results leave through shared memory by TMA: stored from the registers, a
+// row a thread, the 32 lines that each store touches took as long as the
+// products.
 template <typename T, int L>
 __global__ void __launch_bounds__(kExpandThreads, 1)
     latent_expand_kernel(const __grid_constant__ CUtensorMap tm_cache,
                          const __grid_constant__ CUtensorMap tm_weights,
+                         const __grid_constant__ CUtensorMap tm_key,
+                         const __grid_constant__ CUtensorMap tm_value,
                          const __grid_constant__ LatentPrefillArgs a)
 {
     using S = ExpandShape<L>;
@@ -102,7 +108,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* s_rows = smem;
     uint8_t* s_weights = smem + S::kRowsBytes;
-    uint64_t* r_full = reinterpret_cast<uint64_t*>(s_weights + ST * S::kStageBytes);   // [CH]
+    uint8_t* s_out = s_weights + ST * S::kStageBytes;
+    uint64_t* r_full = reinterpret_cast<uint64_t*>(s_out + S::kOutBytes);   // [CH]
     uint64_t* w_full = r_full + CH;        // [ST]
     uint64_t* w_empty = w_full + ST;       // [ST]
     uint64_t* o_full = w_empty + ST;       // [2]
@@ -153,22 +160,23 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         }
         int32_t it = 0;
         for (int h = 0; h < heads && ok; ++h) {
-            for (int c = 0; c < CH && ok; ++c, ++it) {
+            for (int c = 0; c < 2 * CH && ok; ++c, ++it) {       // key and value of each chunk
                 const int st = it % ST;
                 if (it >= ST) ok = mbar_poll_warp(w_empty + st, (it / ST - 1) & 1);
                 if (!ok) break;
                 if (leader) {
                     mbar_arrive_expect_tx(w_full + st, S::kStageBytes);
-                    tma_load_3d(s_weights + st * S::kStageBytes, &tm_weights, c * 64,
-                                (h0 + h) * (kNope + kValue), 0, w_full + st);
+                    tma_load_3d(s_weights + st * S::kStageBytes, &tm_weights, (c >> 1) * 64,
+                                (h0 + h) * (kNope + kValue) + (c & 1) * kNope, 0, w_full + st);
                 }
-                if (h == 0) {                             // the rows, with the first head's weights
-                    if (leader) mbar_arrive_expect_tx(r_full + c, blocks * block_bytes);
+                if (h == 0 && (c & 1) == 0) {             // the rows, with the first head's weights
+                    const int rc = c >> 1;
+                    if (leader) mbar_arrive_expect_tx(r_full + rc, blocks * block_bytes);
                     for (int b = 0; b < blocks; ++b) {
                         const int32_t pg = __shfl_sync(kFullMask, page, b);
                         if (leader)
-                            tma_load_3d(s_rows + c * kKvTile * 128 + b * block_bytes, &tm_cache, c * 64,
-                                        0, pg, r_full + c);
+                            tma_load_3d(s_rows + rc * kKvTile * 128 + b * block_bytes, &tm_cache,
+                                        rc * 64, 0, pg, r_full + rc);
                     }
                 }
             }
@@ -176,10 +184,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         if (!ok) {                                        // let the copies in flight land
             if (lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
             for (int k = max(0, it - ST); k < it; ++k) mbar_poll_warp(w_full + k % ST, (k / ST) & 1);
-            for (int c = 0; c < min(CH, it); ++c) mbar_poll_warp(r_full + c, 0);
+            for (int c = 0; c < min(CH, (it + 1) / 2); ++c) mbar_poll_warp(r_full + c, 0);
         }
     } else if (warp == 5) {
-        const uint32_t idesc = mma_desc<T>(kKvTile, kNope + kValue);
+        const uint32_t idesc = mma_desc<T>(kKvTile, kNope);
         const uint32_t r_addr = smem_u32(s_rows), w_addr = smem_u32(s_weights);
         int32_t it = 0;
         for (int h = 0; h < heads && ok; ++h) {
@@ -187,15 +195,17 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             if (h >= 2) ok = mbar_poll_warp(o_empty + b, (h / 2 - 1) & 1);
             tmem_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < CH && ok; ++c, ++it) {
+            for (int c = 0; c < 2 * CH && ok; ++c, ++it) {
                 const int st = it % ST;
-                ok = mbar_poll_warp(w_full + st, (it / ST) & 1) && (h > 0 || mbar_poll_warp(r_full + c, 0));
+                ok = mbar_poll_warp(w_full + st, (it / ST) & 1) &&
+                     (h > 0 || (c & 1) != 0 || mbar_poll_warp(r_full + (c >> 1), 0));
                 if (!ok) break;
-                const uint64_t da = desc_k_major(r_addr + c * kKvTile * 128);
+                const uint64_t da = desc_k_major(r_addr + (c >> 1) * kKvTile * 128);
                 const uint64_t db = desc_k_major(w_addr + st * S::kStageBytes);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_ss(tmem + b * 256, da + 2 * k, db + 2 * k, idesc, c + k > 0, leader);
+                    mma_ss(tmem + b * 256 + (c & 1) * kNope, da + 2 * k, db + 2 * k, idesc,
+                           (c >> 1) + k > 0, leader);
                 if (leader) mma_commit(w_empty + st);
             }
             if (leader && ok) mma_commit(o_full + b);
@@ -229,32 +239,45 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         for (int h = 0; h < heads; ++h) {
             const int b = h & 1;
-            ok = mbar_poll_warp(o_full + b, (h / 2) & 1);
-            if (!ok) break;
+            // a wait that gave up is not repeated: the warps walk on together, so
+            // that none is left alone at a barrier (PA_STATUS_TIMEOUT)
+            if (ok) ok = mbar_poll_warp(o_full + b, (h / 2) & 1);
             tmem_fence_after();
-            const int64_t row = (static_cast<int64_t>(s) * a.num_heads + h0 + h) * a.rows + t;
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {                 // 32 columns each: four of K, four of V
-                uint32_t o[32];
-                tmem_ld32(o, lanes + b * 256 + c * 32);
+            for (int c = 0; c < 4; ++c) {                 // 64 columns each: two of K, two of V
+                uint32_t o[2][32];
+                tmem_ld32(o[0], lanes + b * 256 + c * 64);
+                tmem_ld32(o[1], lanes + b * 256 + c * 64 + 32);
                 tmem_wait_ld();
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(c < 4 ? a.ws_k : a.ws_v) +
-                                                      row * kNope + (c & 3) * 32);
+                if (c == 3) {
+                    tmem_fence_before();
+                    mbar_arrive(o_empty + b);
+                }
+                // the last box has been read out of shared memory
+                if (r == 0) tma_store_wait_read<0>();
+                named_barrier(1, 128);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 8; ++i) {
                     uint32_t p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        p[e] = Elem<T>::from_float2(__uint_as_float(o[8 * i + 2 * e]),
-                                                    __uint_as_float(o[8 * i + 2 * e + 1]));
+                        p[e] = Elem<T>::from_float2(__uint_as_float(o[i >> 2][8 * (i & 3) + 2 * e]),
+                                                    __uint_as_float(o[i >> 2][8 * (i & 3) + 2 * e + 1]));
                     // a token that does not count is a row of zeros: 0 times what
                     // its place holds may not be 0
-                    dst[i] = counts ? make_uint4(p[0], p[1], p[2], p[3]) : make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(s_out + r * 128 + ((i ^ (r & 7)) << 4)) =
+                        counts ? make_uint4(p[0], p[1], p[2], p[3]) : make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                named_barrier(1, 128);
+                if (r == 0) {
+                    tma_store_3d(c < 2 ? &tm_key : &tm_value, (c & 1) * 64, t0,
+                                 s * a.num_heads + h0 + h, s_out);
+                    tma_store_commit();
                 }
             }
-            tmem_fence_before();
-            mbar_arrive(o_empty + b);
         }
+        if (r == 0) tma_store_wait_all();
         if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
     }
     __syncwarp();
@@ -270,10 +293,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 struct AttendShape {
     static constexpr int kChunks = (kNope + kRot) / 64;
     static constexpr int kQueryBytes = kChunks * kQueryTile * 128;
-    static constexpr int kKeyBytes = kChunks * kKvTile * 128;
-    static constexpr int kValueBytes = kValue / 64 * kKvTile * 128;
-    static constexpr int kKeyStages = 2;
-    static constexpr int kSmem = 1024 + 2 * kQueryBytes + kKeyStages * kKeyBytes + kValueBytes + 512;
+    static constexpr int kSlotBytes = kKvTile * 128;           // 64 columns of a tile of keys or values
+    static constexpr int kKeySlots = kChunks, kValueSlots = kValue / 64;
+    static constexpr int kSlots = 8;                           // of a ring of K and V by turns
+    static constexpr int kSmem = 1024 + 2 * kQueryBytes + kSlots * kSlotBytes + 512;
     // TMEM: S of the two query tiles (P takes the first half of its S), O of both
     static constexpr int kOCol = 256;
 };
@@ -284,6 +307,12 @@ constexpr int kAttendThreads = 320;
 // 0-3 and 4-7 softmax of one query tile each, a thread a query; 8 copies; 9
 // products.  While one tile's scores go through the softmax, the products of
 // the other run.
+//
+// Tile i of the keys takes slots 5 i .. 5 i + 2 of the ring (modulo 8), its
+// values the two after them.  So K_i follows K_{i-2} and V_{i-2}, and V_i
+// follows K_{i-1}, which is free as soon as its scores are taken: the values
+// lie there when their weights are ready.  (With two buffers for K and one for
+// V every step waited 700 cycles for its values.)
 template <typename T>
 __global__ void __launch_bounds__(kAttendThreads, 1)
     latent_attend_kernel(const __grid_constant__ CUtensorMap tm_query,
@@ -297,14 +326,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* s_query = smem;
-    uint8_t* s_key = s_query + 2 * S::kQueryBytes;
-    uint8_t* s_value = s_key + S::kKeyStages * S::kKeyBytes;
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(s_value + S::kValueBytes);    // [2]
-    uint64_t* k_full = q_full + 2;         // [2]
+    uint8_t* s_ring = s_query + 2 * S::kQueryBytes;
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(s_ring + S::kSlots * S::kSlotBytes);    // [2]
+    uint64_t* k_full = q_full + 2;         // [2], of even and odd tiles
     uint64_t* k_empty = k_full + 2;        // [2]
-    uint64_t* v_full = k_empty + 2;
-    uint64_t* v_empty = v_full + 1;
-    uint64_t* s_full = v_empty + 1;        // [2]
+    uint64_t* v_full = k_empty + 2;        // [2]
+    uint64_t* v_empty = v_full + 2;        // [2]
+    uint64_t* s_full = v_empty + 2;        // [2]
     uint64_t* p_full = s_full + 2;         // [2]
     uint64_t* pv_done = p_full + 2;        // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pv_done + 2);
@@ -347,9 +375,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 128);
             mbar_init(pv_done + i, 1);
+            mbar_init(v_full + i, 1);
+            mbar_init(v_empty + i, 1);
         }
-        mbar_init(v_full, 1);
-        mbar_init(v_empty, 1);
         fence_barrier_init();
     }
     if (warp == 9) tmem_alloc(tmem_slot, 512);
@@ -361,17 +389,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     bool ok = true;
 
     if (warp == 8) {
-        auto key = [&](int32_t i) {
-            const int st = i & 1;
-            if (leader) {
-                mbar_arrive_expect_tx(k_full + st, S::kKeyBytes);
-                uint8_t* dst = s_key + st * S::kKeyBytes;
-                tma_load_3d(dst, &tm_key, 0, i * kKvTile, s * a.num_heads + h, k_full + st);
-                tma_load_3d(dst + kKvTile * 128, &tm_key, 64, i * kKvTile, s * a.num_heads + h, k_full + st);
-                tma_load_3d(dst + 2 * kKvTile * 128, &tm_rot, 0, i * kKvTile, s, k_full + st);
-            }
-        };
-        int32_t keys = 0, values = 0;
         if (leader) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -383,41 +400,52 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                                 span.first + row0 + t * kQueryTile, h, q_full + t);
             }
         }
-        key(keys++);
-        for (; values < total; ++values) {
-            if (values > 0) ok = mbar_poll_warp(v_empty, (values - 1) & 1);
+        int32_t keys = 0, values = 0;                     // tiles copied
+        const int32_t plane = s * a.num_heads + h;
+        for (int32_t i = 0; i < total; ++i) {
+            const int b = i & 1;
+            if (i >= 2)
+                ok = mbar_poll_warp(k_empty + b, (i / 2 - 1) & 1) &&
+                     mbar_poll_warp(v_empty + b, (i / 2 - 1) & 1);
             if (!ok) break;
             if (leader) {
-                mbar_arrive_expect_tx(v_full, S::kValueBytes);
+                mbar_arrive_expect_tx(k_full + b, S::kKeySlots * S::kSlotBytes);
 #pragma unroll
-                for (int c = 0; c < kValue / 64; ++c)
-                    tma_load_3d(s_value + c * kKvTile * 128, &tm_value, c * 64, values * kKvTile,
-                                s * a.num_heads + h, v_full);
+                for (int c = 0; c < S::kKeySlots; ++c)
+                    tma_load_3d(s_ring + (5 * i + c) % S::kSlots * S::kSlotBytes,
+                                c < 2 ? &tm_key : &tm_rot, c < 2 ? c * 64 : 0, i * kKvTile,
+                                c < 2 ? plane : s, k_full + b);
             }
-            if (keys < total) {
-                if (keys >= 2) ok = mbar_poll_warp(k_empty + (keys & 1), (keys / 2 - 1) & 1);
-                if (!ok) break;
-                key(keys++);
+            ++keys;
+            if (i >= 1) ok = mbar_poll_warp(k_empty + (b ^ 1), ((i - 1) / 2) & 1);
+            if (!ok) break;
+            if (leader) {
+                mbar_arrive_expect_tx(v_full + b, S::kValueSlots * S::kSlotBytes);
+#pragma unroll
+                for (int c = 0; c < S::kValueSlots; ++c)
+                    tma_load_3d(s_ring + (5 * i + 3 + c) % S::kSlots * S::kSlotBytes, &tm_value, c * 64,
+                                i * kKvTile, plane, v_full + b);
             }
+            ++values;
         }
         if (!ok) {                                        // let the copies in flight land
             if (lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
             for (int t = 0; t < 2; ++t)
                 if (steps[t] > 0) mbar_poll_warp(q_full + t, 0);
             for (int k = max(0, keys - 2); k < keys; ++k) mbar_poll_warp(k_full + (k & 1), (k / 2) & 1);
-            mbar_poll_warp(v_full, (values - 1) & 1);
+            for (int k = max(0, values - 2); k < values; ++k) mbar_poll_warp(v_full + (k & 1), (k / 2) & 1);
         }
     } else if (warp == 9) {
         const uint32_t idesc_s = mma_desc<T>(kQueryTile, kKvTile);
-        const uint32_t idesc_o = mma_desc<T>(kQueryTile, kValue, false, true);
-        const uint32_t q_addr = smem_u32(s_query), k_addr = smem_u32(s_key), v_addr = smem_u32(s_value);
+        const uint32_t idesc_o = mma_desc<T>(kQueryTile, 64, false, true);
+        const uint32_t q_addr = smem_u32(s_query), ring = smem_u32(s_ring);
         auto scores = [&](int t, int32_t i) {
             ok = ok && mbar_poll_warp(k_full + (i & 1), (i / 2) & 1);
             if (!ok) return;
 #pragma unroll
             for (int c = 0; c < S::kChunks; ++c) {
                 const uint64_t da = desc_k_major(q_addr + t * S::kQueryBytes + c * kQueryTile * 128);
-                const uint64_t db = desc_k_major(k_addr + (i & 1) * S::kKeyBytes + c * kKvTile * 128);
+                const uint64_t db = desc_k_major(ring + (5 * i + c) % S::kSlots * S::kSlotBytes);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_ss(tmem + t * kKvTile, da + 2 * k, db + 2 * k, idesc_s, c + k > 0, leader);
@@ -435,20 +463,25 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (i < steps[t] && ok) {
-                    ok = mbar_poll_warp(v_full, i & 1) && mbar_poll_warp(p_full + t, i & 1);
+                    ok = mbar_poll_warp(v_full + (i & 1), (i / 2) & 1) && mbar_poll_warp(p_full + t, i & 1);
                     if (!ok) break;
                     tmem_fence_after();
 #pragma unroll
-                    for (int k = 0; k < kKvTile / 16; ++k)
-                        mma_ts(tmem + S::kOCol + t * kValue, tmem + t * kKvTile + k * 8,
-                               desc_mn_major(v_addr + k * 2048, kKvTile * 128), idesc_o, i + k > 0, leader);
+                    for (int c = 0; c < S::kValueSlots; ++c) {
+                        const uint64_t db = desc_mn_major(
+                            ring + (5 * i + 3 + c) % S::kSlots * S::kSlotBytes, S::kSlotBytes);
+#pragma unroll
+                        for (int k = 0; k < kKvTile / 16; ++k)
+                            mma_ts(tmem + S::kOCol + t * kValue + c * 64, tmem + t * kKvTile + k * 8,
+                                   db + k * (2048 >> 4), idesc_o, i + k > 0, leader);
+                    }
                     if (leader) mma_commit(pv_done + t);
                     // S of the next tile takes the place of P: products run in order
                     if (i + 1 < steps[t]) scores(t, i + 1);
                 }
             }
             if (leader && ok) {
-                mma_commit(v_empty);
+                mma_commit(v_empty + (i & 1));
                 mma_commit(k_empty + ((i + 1) & 1));
             }
         }

@@ -339,4 +339,32 @@ __device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* tensor_m
         : "memory");
 }
 
+// Tiled tensor store shared -> global of one box of a 3-D tensor map (a part
+// outside the tensor is not written).  The writes to shared memory must have
+// been made visible with fence_proxy_async_smem(); the issuing thread closes a
+// group and waits for it before the box's memory is written again.
+__device__ __forceinline__ void tma_store_3d(const void* tensor_map, int x, int y, int z,
+                                             const void* src_smem)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            reinterpret_cast<uint64_t>(tensor_map)),
+        "r"(x), "r"(y), "r"(z), "r"(smem_u32(src_smem))
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_commit()
+{
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until at most N groups of this thread still read shared memory.
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_all()
+{
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 }  // namespace pa
