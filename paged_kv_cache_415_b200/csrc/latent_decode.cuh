@@ -190,6 +190,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         fence_barrier_init();
     }
     if (warp == 5) tmem_alloc(tmem_slot, S::kAlloc);
+    if (warp == 4 && lane == 0) {
+        prefetch_tensor_map(&tm_query);
+        prefetch_tensor_map(&tm_cache);
+    }
     grid_dependency_wait();
     allow_dependents();
 

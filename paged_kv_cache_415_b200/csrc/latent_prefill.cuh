@@ -120,6 +120,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     const int s = blockIdx.z, t0 = blockIdx.y * kKvTile;
     const int h0 = blockIdx.x * a.heads_per_cta;
     const int heads = min(a.heads_per_cta, a.num_heads - h0);
+    if (threadIdx.x == 0) {
+        prefetch_tensor_map(&tm_cache);
+        prefetch_tensor_map(&tm_weights);
+        prefetch_tensor_map(&tm_key);
+        prefetch_tensor_map(&tm_value);
+    }
     grid_dependency_wait();
     const PromptSpan span = prompt_span(a, s);
     allow_dependents();
@@ -301,12 +307,14 @@ struct AttendShape {
     static constexpr int kOCol = 256;
 };
 
-constexpr int kAttendThreads = 320;
+constexpr int kAttendThreads = 352;
 
 // Grid (head, pair of query tiles with the longest first, sequence).  Warps:
 // 0-3 and 4-7 softmax of one query tile each, a thread a query; 8 copies; 9
-// products.  While one tile's scores go through the softmax, the products of
-// the other run.
+// and 10 the products of one query tile each.  While one tile's scores go
+// through the softmax, the products of the other run; with a warp each, one
+// tile's waits do not hold up the other's products (with one warp for both the
+// tensor cores stood still 480 cycles a step).
 //
 // Tile i of the keys takes slots 5 i .. 5 i + 2 of the ring (modulo 8), its
 // values the two after them.  So K_i follows K_{i-2} and V_{i-2}, and V_i
@@ -336,10 +344,17 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     uint64_t* p_full = s_full + 2;         // [2]
     uint64_t* pv_done = p_full + 2;        // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pv_done + 2);
+    int32_t* begun = reinterpret_cast<int32_t*>(tmem_slot + 1);   // the first tile's first weights
 
     const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int h = blockIdx.x, s = blockIdx.z;
     const int row0 = (gridDim.y - 1 - blockIdx.y) * 2 * kQueryTile;
+    if (threadIdx.x == 0) {
+        prefetch_tensor_map(&tm_query);
+        prefetch_tensor_map(&tm_key);
+        prefetch_tensor_map(&tm_value);
+        prefetch_tensor_map(&tm_rot);
+    }
     grid_dependency_wait();
     const PromptSpan span = prompt_span(a, s);
     if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0 && (span.first < 0 || span.context < 0))
@@ -371,13 +386,14 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full + i, 1);
             mbar_init(k_full + i, 1);
-            mbar_init(k_empty + i, 1);
+            mbar_init(k_empty + i, 2);                    // both tiles' products
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 128);
             mbar_init(pv_done + i, 1);
             mbar_init(v_full + i, 1);
-            mbar_init(v_empty + i, 1);
+            mbar_init(v_empty + i, 2);
         }
+        *begun = 0;
         fence_barrier_init();
     }
     if (warp == 9) tmem_alloc(tmem_slot, 512);
@@ -389,17 +405,15 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     bool ok = true;
 
     if (warp == 8) {
-        if (leader) {
+        auto queries = [&](int t) {
+            if (steps[t] == 0 || !leader) return;
+            mbar_arrive_expect_tx(q_full + t, S::kQueryBytes);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (steps[t] == 0) continue;
-                mbar_arrive_expect_tx(q_full + t, S::kQueryBytes);
-#pragma unroll
-                for (int c = 0; c < S::kChunks; ++c)
-                    tma_load_3d(s_query + t * S::kQueryBytes + c * kQueryTile * 128, &tm_query, c * 64,
-                                span.first + row0 + t * kQueryTile, h, q_full + t);
-            }
-        }
+            for (int c = 0; c < S::kChunks; ++c)
+                tma_load_3d(s_query + t * S::kQueryBytes + c * kQueryTile * 128, &tm_query, c * 64,
+                            span.first + row0 + t * kQueryTile, h, q_full + t);
+        };
+        queries(0);                                       // the second tile's after the first keys
         int32_t keys = 0, values = 0;                     // tiles copied
         const int32_t plane = s * a.num_heads + h;
         for (int32_t i = 0; i < total; ++i) {
@@ -417,6 +431,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                                 c < 2 ? plane : s, k_full + b);
             }
             ++keys;
+            if (i == 0) queries(1);
             if (i >= 1) ok = mbar_poll_warp(k_empty + (b ^ 1), ((i - 1) / 2) & 1);
             if (!ok) break;
             if (leader) {
@@ -435,55 +450,67 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             for (int k = max(0, keys - 2); k < keys; ++k) mbar_poll_warp(k_full + (k & 1), (k / 2) & 1);
             for (int k = max(0, values - 2); k < values; ++k) mbar_poll_warp(v_full + (k & 1), (k / 2) & 1);
         }
-    } else if (warp == 9) {
+    } else if (warp >= 9) {
+        const int t = warp - 9;
+        const int32_t n = steps[t];
         const uint32_t idesc_s = mma_desc<T>(kQueryTile, kKvTile);
         const uint32_t idesc_o = mma_desc<T>(kQueryTile, 64, false, true);
-        const uint32_t q_addr = smem_u32(s_query), ring = smem_u32(s_ring);
-        auto scores = [&](int t, int32_t i) {
-            ok = ok && mbar_poll_warp(k_full + (i & 1), (i / 2) & 1);
-            if (!ok) return;
+        const uint32_t query = smem_u32(s_query) + t * S::kQueryBytes, ring = smem_u32(s_ring);
+        // Scores of tile i of the keys, which has arrived; past the tile's last
+        // step the room is let go of all the same (not before the keys are
+        // there: a release a step, or the copies would run ahead).
+        auto scores = [&](int32_t i) {
+            if (i >= n) {
+                if (leader) mbar_arrive(k_empty + (i & 1));
+                return;
+            }
 #pragma unroll
             for (int c = 0; c < S::kChunks; ++c) {
-                const uint64_t da = desc_k_major(q_addr + t * S::kQueryBytes + c * kQueryTile * 128);
+                const uint64_t da = desc_k_major(query + c * kQueryTile * 128);
                 const uint64_t db = desc_k_major(ring + (5 * i + c) % S::kSlots * S::kSlotBytes);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mma_ss(tmem + t * kKvTile, da + 2 * k, db + 2 * k, idesc_s, c + k > 0, leader);
             }
-            if (leader) mma_commit(s_full + t);
+            if (leader) {
+                mma_commit(s_full + t);
+                mma_commit(k_empty + (i & 1));
+            }
         };
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            if (steps[t] == 0) continue;
-            ok = ok && mbar_poll_warp(q_full + t, 0);
-            scores(t, 0);
-        }
-        if (leader && ok) mma_commit(k_empty);
+        ok = (n == 0 || mbar_poll_warp(q_full + t, 0)) && mbar_poll_warp(k_full, 0);
+        // The second tile starts when the first one's weights are out: half a
+        // step apart their softmax and products alternate; side by side they
+        // stayed so for ten steps, 5400 cycles each instead of 3700.
+        if (t == 1 && n > 0)
+            for (int i = 0; i < 4096 && !__all_sync(kFullMask, *static_cast<volatile int32_t*>(begun) != 0); ++i)
+                __nanosleep(20);
+        if (ok) scores(0);
         for (int32_t i = 0; i < total && ok; ++i) {
+            // values and next keys are looked for before the weights: they are there first
+            ok = mbar_poll_warp(v_full + (i & 1), (i / 2) & 1) &&
+                 (i + 1 >= total || mbar_poll_warp(k_full + ((i + 1) & 1), ((i + 1) / 2) & 1)) &&
+                 (i >= n || mbar_poll_warp(p_full + t, i & 1));
+            if (!ok) break;
+            tmem_fence_after();
+            if (i < n) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (i < steps[t] && ok) {
-                    ok = mbar_poll_warp(v_full + (i & 1), (i / 2) & 1) && mbar_poll_warp(p_full + t, i & 1);
-                    if (!ok) break;
-                    tmem_fence_after();
+                for (int c = 0; c < S::kValueSlots; ++c) {
+                    const uint64_t db = desc_mn_major(
+                        ring + (5 * i + 3 + c) % S::kSlots * S::kSlotBytes, S::kSlotBytes);
 #pragma unroll
-                    for (int c = 0; c < S::kValueSlots; ++c) {
-                        const uint64_t db = desc_mn_major(
-                            ring + (5 * i + 3 + c) % S::kSlots * S::kSlotBytes, S::kSlotBytes);
-#pragma unroll
-                        for (int k = 0; k < kKvTile / 16; ++k)
-                            mma_ts(tmem + S::kOCol + t * kValue + c * 64, tmem + t * kKvTile + k * 8,
-                                   db + k * (2048 >> 4), idesc_o, i + k > 0, leader);
-                    }
-                    if (leader) mma_commit(pv_done + t);
-                    // S of the next tile takes the place of P: products run in order
-                    if (i + 1 < steps[t]) scores(t, i + 1);
+                    for (int k = 0; k < kKvTile / 16; ++k)
+                        mma_ts(tmem + S::kOCol + t * kValue + c * 64, tmem + t * kKvTile + k * 8,
+                               db + k * (2048 >> 4), idesc_o, i + k > 0, leader);
                 }
+                if (leader) {
+                    mma_commit(pv_done + t);
+                    mma_commit(v_empty + (i & 1));
+                }
+            } else if (leader) {
+                mbar_arrive(v_empty + (i & 1));
             }
-            if (leader && ok) {
-                mma_commit(v_empty + (i & 1));
-                mma_commit(k_empty + ((i + 1) & 1));
-            }
+            // S of the next tile takes the place of P: products run in order
+            if (i + 1 < total) scores(i + 1);
         }
         if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
     } else {
@@ -522,8 +549,9 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < kKvTile; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e]));
-            const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
+            for (int e = 0; e < kKvTile; e += 2)
+                top[e >> 1 & 3] = max3(top[e >> 1 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            const float peak = max3(top[0], top[1], fmaxf(top[2], top[3])) * unit;
             // The reference moves where it is unset or passed by 2^8.
             const bool moves = peak > m + 8.0f;
             if (__any_sync(kFullMask, moves)) {
@@ -547,47 +575,62 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 }
             }
             const float sub = m == -INFINITY ? 0.f : m;
-            float sum[2] = {0.f, 0.f};
+            float2 sum = make_float2(0.f, 0.f);
+            const float2 unit2 = make_float2(unit, unit), sub2 = make_float2(-sub, -sub);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t p[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
-                    const float p0 = exp2_fast(fmaf(__uint_as_float(x[64 * c + 2 * e]), unit, -sub));
-                    const float p1 = exp2_fast(fmaf(__uint_as_float(x[64 * c + 2 * e + 1]), unit, -sub));
-                    sum[0] += p0;
-                    sum[1] += p1;
-                    p[e] = Elem<T>::from_float2(p0, p1);
+                    const float2 y = fma2(make_float2(__uint_as_float(x[64 * c + 2 * e]),
+                                                      __uint_as_float(x[64 * c + 2 * e + 1])), unit2, sub2);
+                    const float2 w = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                    sum = add2(sum, w);
+                    p[e] = Elem<T>::from_float2(w.x, w.y);
                 }
                 tmem_st32(s_tmem + 32 * c, p);
             }
-            l += sum[0] + sum[1];
+            l += sum.x + sum.y;
             tmem_wait_st();
             tmem_fence_before();
             mbar_arrive(p_full + t);
+            if (i == 0 && threadIdx.x == 0) *static_cast<volatile int32_t*>(begun) = 1;
         }
         if (ok && n > 0) ok = mbar_poll_warp(pv_done + t, (n - 1) & 1);
         if (ok && n > 0) {
             tmem_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            T* dst = static_cast<T*>(a.out) +
-                     (static_cast<int64_t>(span.first + min(r, span.count - 1)) * a.num_heads + h) * kValue;
-#pragma unroll 1
+            // Through shared memory (the tile's queries have been used), 8 KB a
+            // warp: stored a row a thread, the 32 lines that each store touches
+            // took 9000 cycles.  16-byte chunk j of row r lies at j ^ (r % 8).
+            uint8_t* mine = s_query + t * S::kQueryBytes + (warp & 3) * 8192;
+#pragma unroll
             for (int c = 0; c < kValue; c += 32) {
                 uint32_t o[32];
                 tmem_ld32(o, o_tmem + c);
                 tmem_wait_ld();
-                if (r < span.count) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t p[4];
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t p[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            p[e] = Elem<T>::from_float2(__uint_as_float(o[8 * j + 2 * e]) * inv,
-                                                        __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
-                        reinterpret_cast<uint4*>(dst + c)[j] = make_uint4(p[0], p[1], p[2], p[3]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        p[e] = Elem<T>::from_float2(__uint_as_float(o[8 * j + 2 * e]) * inv,
+                                                    __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
+                    *reinterpret_cast<uint4*>(mine + lane * 256 + ((c / 8 + j) ^ (lane & 7)) * 16) =
+                        make_uint4(p[0], p[1], p[2], p[3]);
                 }
+            }
+            __syncwarp();
+            const int32_t first = row0 + t * kQueryTile + (warp & 3) * 32;      // the warp's first query
+            T* dst = static_cast<T*>(a.out) +
+                     (static_cast<int64_t>(span.first + first) * a.num_heads + h) * kValue + (lane & 15) * 8;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const int row = 2 * k + (lane >> 4);
+                const uint4 v =
+                    *reinterpret_cast<const uint4*>(mine + row * 256 + ((lane & 15) ^ (row & 7)) * 16);
+                if (first + row < span.count)
+                    *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(row) * a.num_heads * kValue) = v;
             }
         }
         if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
