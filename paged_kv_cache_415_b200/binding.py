@@ -151,6 +151,8 @@ def _load() -> ctypes.CDLL:
 
 LIB = _load()
 
+from . import _marshal  # noqa: E402  (built beside libpa.so; no fallback)
+
 
 def _ptr(t) -> int | None:
     if t is None:
@@ -517,45 +519,19 @@ def pa_swap_blocks(src_k, src_v, dst_k, dst_v, block_mapping, d_status=None, str
 # ---------------------------------------------------------------------------
 # Appends with norm and rotation, and the latent pool.  These calls take
 # tensors with strides and of several types, so what the library cannot see
-# from the pointers (element types, strides, devices) is checked here.
+# from the pointers (element types, shapes, strides, devices) is checked, and
+# refused with ValueError, before the C call: in _marshal (csrc_py/marshal.cpp),
+# where that costs well under a microsecond.  The device of the tensors is made
+# current for the call; without a stream it goes to that device's current one.
 # ---------------------------------------------------------------------------
 
-def _need(fn: str, ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(f"{fn}: {what}")
+def _bind_marshal(lib):
+    address = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+    _marshal.bind(address("pa_rope_append"), address("pa_latent_append"),
+                  address("pa_latent_decode"), address("pa_latent_prefill"))
 
 
-def _launch(fn: str, like: torch.Tensor, stream, *args) -> None:
-    """The C call on `stream`, or on the current stream of `like`'s device,
-    with that device current."""
-    index = like.device.index
-    if index == torch.cuda.current_device():
-        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
-        code = getattr(LIB, fn)(*args, s)
-    else:
-        with torch.cuda.device(index):
-            s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
-            code = getattr(LIB, fn)(*args, s)
-    if code != PA_OK:
-        raise PAError(fn, code)
-
-
-def _need_vector(fn, t, n, dtype, name):
-    _need(fn, t.dtype == dtype and t.dim() == 1 and t.shape[0] == n and t.is_contiguous(),
-          f"{name} must be a contiguous {dtype} tensor of {n} elements")
-
-
-def _need_rows(fn, t, rows, heads, dim, dtype, name):
-    """[rows][heads][dim] with whole head rows side by side; the tokens' stride is free."""
-    _need(fn, t.dtype == dtype and t.shape == (rows, heads, dim) and t.stride(2) == 1
-          and (t.stride(1) == dim or heads == 1),
-          f"{name} must be {dtype} [{rows}][{heads}][{dim}] with contiguous heads")
-
-
-def _need_same_device(fn, like, *tensors):
-    dev = like.device
-    _need(fn, dev.type == "cuda" and all(t is None or t.device == dev for t in tensors),
-          "all tensors must be on one CUDA device")
+_bind_marshal(LIB)
 
 
 def pa_rope_append(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions,
@@ -568,39 +544,12 @@ def pa_rope_append(query_out, query, key, value, k_cache, v_cache, slot_mapping,
     [num_blocks][B][Hkv][D] of the same type or one-byte codes (k_scale /
     v_scale, or scale pools k_scales / v_scales); slot_mapping, positions
     int64 [T]; cos_sin fp32 [max_position][rot_dim]."""
-    fn = "pa_rope_append"
-    num_tokens, hq, d = query.shape
-    num_blocks, block_size, hkv, _ = k_cache.shape
-    dt = query.dtype
-    _need_rows(fn, query, num_tokens, hq, d, dt, "query")
-    _need_rows(fn, query_out, num_tokens, hq, d, dt, "query_out")
-    _need_rows(fn, key, num_tokens, hkv, d, dt, "key")
-    _need_rows(fn, value, num_tokens, hkv, d, dt, "value")
-    _need(fn, k_cache.shape == v_cache.shape and k_cache.shape[3] == d
-          and k_cache.dtype == v_cache.dtype and k_cache.is_contiguous()
-          and v_cache.is_contiguous(), "k_cache and v_cache must be contiguous pools of one shape")
-    _need_vector(fn, slot_mapping, num_tokens, torch.int64, "slot_mapping")
-    _need_vector(fn, positions, num_tokens, torch.int64, "positions")
-    _need(fn, cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
-          "cos_sin must be contiguous float32 [max_position][rot_dim]")
-    for w in (q_weight, k_weight):
-        if w is not None:
-            _need_vector(fn, w, d, dt, "a norm weight")
-    for s in (k_scales, v_scales):
-        _need(fn, s is None or (s.dtype == torch.float32 and s.is_contiguous()
-                                and s.shape == (num_blocks, hkv, block_size)),
-              "scale pools must be contiguous float32 [num_blocks][Hkv][B]")
-    _need(fn, d_status is None or d_status.dtype == torch.int32, "d_status must be int32")
-    _need_same_device(fn, query, query_out, key, value, k_cache, v_cache, slot_mapping, positions,
-                      cos_sin, q_weight, k_weight, k_scales, v_scales, d_status)
-    _launch(fn, query, stream,
-            query_out.data_ptr(), query.data_ptr(), key.data_ptr(), value.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scales), _ptr(v_scales),
-            slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), _ptr(q_weight),
-            _ptr(k_weight), eps, num_tokens, hq, hkv, d, cos_sin.shape[1], cos_sin.shape[0],
-            1 if interleaved else 0, query_out.stride(0), query.stride(0), key.stride(0),
-            value.stride(0), block_size, num_blocks, _dtype(query), _dtype(k_cache), k_scale,
-            v_scale, _ptr(d_status))
+    code = _marshal.rope_append(query_out, query, key, value, k_cache, v_cache, slot_mapping,
+                                positions, cos_sin, q_weight, k_weight, eps, interleaved, k_scale,
+                                v_scale, k_scales, v_scales, d_status,
+                                -1 if stream is None else _stream(stream))
+    if code != PA_OK:
+        raise PAError("pa_rope_append", code)
 
 
 def pa_latent_append(query_out, query_rope, latent, cache, slot_mapping, positions, cos_sin,
@@ -610,37 +559,11 @@ def pa_latent_append(query_out, query_rope, latent, cache, slot_mapping, positio
     rotate the queries' rotated part.  latent [T][L + R] (any token stride);
     query_rope / query_out [T][H][R] views with any token and head stride, or
     both None; cos_sin fp32 [max_position][R]."""
-    fn = "pa_latent_append"
-    num_blocks, block_size, width = cache.shape
-    num_tokens = latent.shape[0]
-    rope = cos_sin.shape[1]
-    dt = cache.dtype
-    _need(fn, cache.is_contiguous(), "cache must be contiguous")
-    _need(fn, latent.dtype == dt and latent.shape == (num_tokens, width) and latent.stride(1) == 1,
-          f"latent must be {dt} [{num_tokens}][{width}] with contiguous rows")
-    _need(fn, (query_rope is None) == (query_out is None), "query_rope and query_out go together")
-    heads = q_t = q_h = o_t = o_h = 0
-    if query_rope is not None:
-        heads = query_rope.shape[1]
-        for t, name in ((query_rope, "query_rope"), (query_out, "query_out")):
-            _need(fn, t.dtype == dt and t.shape == (num_tokens, heads, rope) and t.stride(2) == 1,
-                  f"{name} must be {dt} [{num_tokens}][{heads}][{rope}] with contiguous rows")
-        q_t, q_h = query_rope.stride(0), query_rope.stride(1)
-        o_t, o_h = query_out.stride(0), query_out.stride(1)
-    _need_vector(fn, slot_mapping, num_tokens, torch.int64, "slot_mapping")
-    _need_vector(fn, positions, num_tokens, torch.int64, "positions")
-    _need(fn, cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
-          "cos_sin must be contiguous float32 [max_position][rope_dim]")
-    if weight is not None:
-        _need_vector(fn, weight, width - rope, dt, "weight")
-    _need(fn, d_status is None or d_status.dtype == torch.int32, "d_status must be int32")
-    _need_same_device(fn, cache, latent, query_rope, query_out, slot_mapping, positions, cos_sin,
-                      weight, d_status)
-    _launch(fn, cache, stream, _ptr(query_out), _ptr(query_rope), latent.data_ptr(),
-            cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(),
-            _ptr(weight), eps, num_tokens, heads, width - rope, rope, cos_sin.shape[0],
-            1 if interleaved else 0, o_t, o_h, q_t, q_h, latent.stride(0), block_size, num_blocks,
-            _dtype(cache), _ptr(d_status))
+    code = _marshal.latent_append(query_out, query_rope, latent, cache, slot_mapping, positions,
+                                  cos_sin, weight, eps, interleaved, d_status,
+                                  -1 if stream is None else _stream(stream))
+    if code != PA_OK:
+        raise PAError("pa_latent_append", code)
 
 
 def pa_latent_decode_workspace_size(num_seqs, num_heads, latent_dim, block_size,
@@ -649,36 +572,17 @@ def pa_latent_decode_workspace_size(num_seqs, num_heads, latent_dim, block_size,
                                                    max_context_len))
 
 
-def _need_tables(fn, block_tables, context_lens, num_seqs):
-    _need(fn, block_tables.dtype == torch.int32 and block_tables.dim() == 2
-          and block_tables.shape[0] == num_seqs and block_tables.is_contiguous(),
-          f"block_tables must be contiguous int32 [{num_seqs}][max_blocks_per_seq]")
-    _need_vector(fn, context_lens, num_seqs, torch.int32, "context_lens")
-
-
 def pa_latent_decode(out, query, cache, block_tables, context_lens, max_context_len, scale,
                      workspace=None, d_status=None, stream=None) -> None:
     """Single-query attention over the latent pool, projections absorbed.
     out [S][H][L], query [S][H][L + R], cache [num_blocks][B][L + R];
     workspace: a uint8 device tensor of at least
     pa_latent_decode_workspace_size(...) bytes (or None when that is 0)."""
-    fn = "pa_latent_decode"
-    num_seqs, heads, width = query.shape
-    num_blocks, block_size, cache_width = cache.shape
-    latent = out.shape[2]
-    _need(fn, query.dtype == cache.dtype == out.dtype and cache_width == width
-          and out.shape[:2] == query.shape[:2] and query.is_contiguous() and cache.is_contiguous()
-          and out.is_contiguous(),
-          "out [S][H][L], query [S][H][L + R] and cache [num_blocks][B][L + R] must be contiguous "
-          "tensors of one type")
-    _need_tables(fn, block_tables, context_lens, num_seqs)
-    _need(fn, d_status is None or d_status.dtype == torch.int32, "d_status must be int32")
-    _need_same_device(fn, query, out, cache, block_tables, context_lens, workspace, d_status)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _launch(fn, query, stream, out.data_ptr(), query.data_ptr(), cache.data_ptr(),
-            block_tables.data_ptr(), context_lens.data_ptr(), num_seqs, heads, latent,
-            width - latent, block_size, block_tables.shape[1], num_blocks, max_context_len, scale,
-            _ptr(workspace), ws_bytes, _dtype(query), _ptr(d_status))
+    code = _marshal.latent_decode(out, query, cache, block_tables, context_lens, max_context_len,
+                                  scale, workspace, d_status,
+                                  -1 if stream is None else _stream(stream))
+    if code != PA_OK:
+        raise PAError("pa_latent_decode", code)
 
 
 def pa_latent_prefill_workspace_size(num_seqs, num_heads, latent_dim, block_size,
@@ -695,31 +599,11 @@ def pa_latent_prefill(out, query, cache, w_kv, block_tables, query_starts, conte
     [T][H][value], query [T][H][nope + R], query_starts int32 [S + 1];
     workspace: a uint8 device tensor of at least
     pa_latent_prefill_workspace_size(...) bytes."""
-    fn = "pa_latent_prefill"
-    num_tokens, heads, q_width = query.shape
-    num_blocks, block_size, width = cache.shape
-    value = out.shape[2]
-    latent = w_kv.shape[2]
-    rope = width - latent
-    nope = q_width - rope
-    _need(fn, query.dtype == cache.dtype == out.dtype == w_kv.dtype
-          and out.shape[:2] == query.shape[:2] and w_kv.shape == (heads, nope + value, latent)
-          and query.is_contiguous() and cache.is_contiguous() and out.is_contiguous()
-          and w_kv.is_contiguous(),
-          "out [T][H][value], query [T][H][nope + R], cache [num_blocks][B][L + R] and w_kv "
-          "[H][nope + value][L] must be contiguous tensors of one type")
-    num_seqs = context_lens.shape[0]
-    _need_tables(fn, block_tables, context_lens, num_seqs)
-    _need_vector(fn, query_starts, num_seqs + 1, torch.int32, "query_starts")
-    _need(fn, d_status is None or d_status.dtype == torch.int32, "d_status must be int32")
-    _need_same_device(fn, query, out, cache, w_kv, block_tables, query_starts, context_lens,
-                      workspace, d_status)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _launch(fn, query, stream, out.data_ptr(), query.data_ptr(), cache.data_ptr(),
-            w_kv.data_ptr(), block_tables.data_ptr(), query_starts.data_ptr(),
-            context_lens.data_ptr(), num_seqs, num_tokens, heads, latent, rope, nope, value,
-            block_size, block_tables.shape[1], num_blocks, max_query_len, max_context_len, scale,
-            _ptr(workspace), ws_bytes, _dtype(query), _ptr(d_status))
+    code = _marshal.latent_prefill(out, query, cache, w_kv, block_tables, query_starts,
+                                   context_lens, max_query_len, max_context_len, scale, workspace,
+                                   d_status, -1 if stream is None else _stream(stream))
+    if code != PA_OK:
+        raise PAError("pa_latent_prefill", code)
 
 
 # ---------------------------------------------------------------------------

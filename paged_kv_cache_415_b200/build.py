@@ -1,10 +1,12 @@
-"""Build libpa.so (the C-ABI CUDA library) in place, for sm_100a.
+"""Build libpa.so (the C-ABI CUDA library) and _marshal.so (the torch side of
+the calls that take strided tensors) in place, for sm_100a.
 
     python -m paged_kv_cache_415_b200.build [--force]
 
 Each .cu file under csrc/ is compiled by nvcc in parallel
 (-gencode arch=compute_100a,code=sm_100a -O3 -lineinfo, no fast-math) and
 linked with the static CUDA runtime into paged_kv_cache_415_b200/libpa.so.
+csrc_py/marshal.cpp is compiled by g++ against torch's headers.
 """
 from __future__ import annotations
 
@@ -14,12 +16,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpa.so")
+MARSHAL_SOURCE = os.path.join(HERE, "csrc_py", "marshal.cpp")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 NVCC_FLAGS = [
@@ -49,14 +54,49 @@ def _deps():
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(target, deps) -> bool:
+    if not os.path.exists(target):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def build_marshal(force: bool = False) -> str:
+    """_marshal.so, a CPython extension over torch's tensors."""
+    deps = [MARSHAL_SOURCE, os.path.join(INCLUDE, "pa.h"), os.path.abspath(__file__)]
+    if not force and _newer(MARSHAL, deps):
+        return MARSHAL
+    import torch
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    root = os.path.dirname(torch.__file__)
+    lib, inc = os.path.join(root, "lib"), os.path.join(root, "include")
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
+           "-isystem" + inc, "-isystem" + os.path.join(inc, "torch", "csrc", "api", "include"),
+           MARSHAL_SOURCE, "-o", tmp, "-L" + lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {MARSHAL_SOURCE}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        marshal = ex.submit(build_marshal, force)
+        lib = _build_library(force, verbose)
+        marshal.result()
+    return lib
+
+
+def _build_library(force: bool, verbose: bool) -> str:
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()
