@@ -355,13 +355,19 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         prefetch_tensor_map(&tm_value);
         prefetch_tensor_map(&tm_rot);
     }
-    grid_dependency_wait();
+    // The expansion lets this launch begin once it has seen all earlier work
+    // complete, so what the caller wrote may be read at once; only what the
+    // expansion writes (the workspace) is waited for.  Every block waits before
+    // it ends, so this launch never completes before the expansion.
     const PromptSpan span = prompt_span(a, s);
     if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0 && (span.first < 0 || span.context < 0))
         status_or(a.d_status, PA_STATUS_BAD_CONTEXT);
-    allow_dependents();
-    if (row0 >= span.count) return;
+    if (row0 >= span.count) {
+        grid_dependency_wait();
+        return;
+    }
     if (span.context < 0) {                               // zero rows
+        grid_dependency_wait();
         const int n = min(2 * kQueryTile, span.count - row0);
         for (int i = threadIdx.x; i < n * (kValue / 8); i += kAttendThreads) {
             const int64_t row = static_cast<int64_t>(span.first + row0 + i / (kValue / 8)) * a.num_heads + h;
@@ -414,6 +420,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             span.first + row0 + t * kQueryTile, h, q_full + t);
         };
         queries(0);                                       // the second tile's after the first keys
+        grid_dependency_wait();
+        allow_dependents();
         int32_t keys = 0, values = 0;                     // tiles copied
         const int32_t plane = s * a.num_heads + h;
         for (int32_t i = 0; i < total; ++i) {
@@ -522,6 +530,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + quarter + t * kKvTile;
         const uint32_t o_tmem = tmem + quarter + S::kOCol + t * kValue;
+        grid_dependency_wait();                           // the masks are the expansion's
         float m = -INFINITY, l = 0.f;
         for (int32_t i = 0; i < n; ++i) {
             const int32_t t0 = i * kKvTile;

@@ -27,6 +27,7 @@ namespace pa {
 
 constexpr int kRopeThreads = 128;
 
+
 struct RopeArgs {
     void* query_out;
     const void* query;
@@ -42,6 +43,7 @@ struct RopeArgs {
     const void* q_weight;             // norm weights [D], or null: no norm
     const void* k_weight;
     float eps;
+    uint32_t num_tokens, per_token;   // lane groups a token
     int32_t num_q_heads, num_kv_heads, rot_dim;
     int64_t max_position;
     int32_t interleaved;
@@ -54,31 +56,32 @@ struct RopeArgs {
 
 struct PlainRows {};                  // pools of the input's own 16-bit type
 
-// Rows of one token a lane group handles, all their loads issued first:
-// kManyRows when the grid is deep enough to fill the GPU without the extra
-// groups (the angles are then loaded once for several heads), else 1.
-constexpr int kManyRows = 4;
-
-// Grid (token, chunk of the token's Hq + 2 Hkv rows).
+// The rows of all tokens, Hq + 2 Hkv each, are shared out over lane groups of
+// D / 8 lanes: `per_token` groups a token, group g taking its rows g, g +
+// per_token, ... (ROWS of them, all loads issued first, the angles loaded once).
+// Neighbouring groups take neighbouring rows, and a warp may hold groups of
+// several tokens, so no lane is idle whatever the head counts.
 template <typename T, typename Store, int D, int ROWS>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs a)
 {
     constexpr int LANES = D / 8;
-    constexpr int kGroups = kRopeThreads / LANES;
     grid_dependency_wait();
     allow_dependents();
-    const int64_t t = blockIdx.x;
-    const int j = threadIdx.x % LANES;            // place in the row
-    const int e0 = j * 8;
-    const int row0 = blockIdx.y * kGroups * ROWS + threadIdx.x / LANES;
     const int hq = a.num_q_heads, hkv = a.num_kv_heads;
     const int rows = hq + 2 * hkv;
+    const int j = threadIdx.x % LANES;            // place in the row
+    const int e0 = j * 8;
+    const uint32_t group = (blockIdx.x * kRopeThreads + threadIdx.x) / LANES;
+    const uint32_t token = group / a.per_token;
+    const int g = static_cast<int>(group - token * a.per_token);
+    const bool inside = token < a.num_tokens;
+    const int64_t t = inside ? token : 0;
     const int64_t pos = a.positions[t];
     const int64_t slot = a.slot_mapping[t];
     uint4 x[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int r = row0 + i * kGroups;
+        const int r = inside ? g + i * static_cast<int>(a.per_token) : rows;
         x[i] = make_uint4(0, 0, 0, 0);
         if (r < hq)
             x[i] = ld_stream_v4(static_cast<const T*>(a.query) + t * a.query_stride +
@@ -90,20 +93,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
             x[i] = ld_stream_v4(static_cast<const T*>(a.value) + t * a.value_stride +
                                 static_cast<int64_t>(r - hq - hkv) * D + e0);
     }
-    if (pos < 0) return;                          // padding token
-    const bool first = blockIdx.y == 0 && threadIdx.x == 0;
-    if (pos >= a.max_position) {
-        if (first) status_or(a.d_status, PA_STATUS_BAD_POSITION);
-        return;
+    // nothing of a padding token (pos < 0) or one past the table is written
+    const bool live = inside && pos >= 0 && pos < a.max_position;
+    const bool cached = live && slot >= 0 && slot < a.num_slots;
+    if (inside && g == 0 && j == 0) {
+        if (pos >= a.max_position) status_or(a.d_status, PA_STATUS_BAD_POSITION);
+        if (live && slot >= a.num_slots) status_or(a.d_status, PA_STATUS_BAD_SLOT);
     }
-    if (slot >= a.num_slots && first) status_or(a.d_status, PA_STATUS_BAD_SLOT);
-    const bool cached = slot >= 0 && slot < a.num_slots;
     Angles ang;
-    if (e0 < a.rot_dim)
+    if (live && e0 < a.rot_dim)
         load_angles(ang, a.cos_sin + pos * a.rot_dim, e0, a.rot_dim, a.interleaved != 0);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-        const int r = row0 + i * kGroups;
+        const int r = g + i * static_cast<int>(a.per_token);
         const bool is_q = r < hq;
         const bool is_k = !is_q && r < hq + hkv;
         float f[8];
@@ -123,16 +125,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
                     for (int e = 0; e < 8; ++e) f[e] = f[e] * rs * wf[e];
                 }
             }
-            float g[8];
+            float g8[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = f[e];
-            rotate8(g, ang, e0, a.rot_dim, a.interleaved != 0);
+            for (int e = 0; e < 8; ++e) g8[e] = f[e];
+            rotate8(g8, ang, e0, a.rot_dim, a.interleaved != 0);
             if (is_q || is_k) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = g[e];
+                for (int e = 0; e < 8; ++e) f[e] = g8[e];
             }
         }
-        if (is_q)
+        if (is_q && live)
             *reinterpret_cast<uint4*>(static_cast<T*>(a.query_out) + t * a.query_out_stride +
                                       static_cast<int64_t>(r) * D + e0) = pack8<T>(f);
         const bool store = !is_q && r < rows && cached;
@@ -172,40 +174,48 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
     }
 }
 
-// Lane groups of a launch below which each takes one row: two waves of full
-// SMs of 64 warps.
-constexpr int64_t kFillWarps = 148 * 64 * 2;
+// Rows a lane group takes: as many (1, 2 or 4) as leave enough warps to fill
+// the GPU, kFillWarps.
+constexpr int64_t kFillWarps = 148 * 32;
 
-template <typename T, typename Store, int D>
-static pa_status launch_rope(const RopeArgs& a, int32_t num_tokens, pa_stream_t stream)
+template <typename T, typename Store, int D, int ROWS>
+static pa_status launch_rope_rows(RopeArgs& a, pa_stream_t stream)
 {
-    constexpr int kGroups = kRopeThreads / (D / 8);
     const int64_t rows = static_cast<int64_t>(a.num_q_heads) + 2 * a.num_kv_heads;
-    const bool many = num_tokens * rows * (D / 8) / 32 >= kFillWarps;
-    const int64_t per_cta = kGroups * (many ? kManyRows : 1);
-    const int64_t chunks = (rows + per_cta - 1) / per_cta;
-    if (chunks > 65535) return PA_ERR_UNSUPPORTED;
-    auto kernel = many ? rope_append_kernel<T, Store, D, kManyRows> : rope_append_kernel<T, Store, D, 1>;
-    return launch_overlapped(kernel, dim3(num_tokens, static_cast<unsigned>(chunks)),
+    const int64_t per_token = (rows + ROWS - 1) / ROWS;
+    const int64_t groups = per_token * a.num_tokens;
+    const int64_t ctas = (groups * (D / 8) + kRopeThreads - 1) / kRopeThreads;
+    // (thread numbers stay below 2^32)
+    if (ctas > 0xffffffffLL / kRopeThreads) return PA_ERR_UNSUPPORTED;
+    a.per_token = static_cast<uint32_t>(per_token);
+    return launch_overlapped(rope_append_kernel<T, Store, D, ROWS>, dim3(static_cast<unsigned>(ctas)),
                              dim3(kRopeThreads), 0, stream, a);
 }
 
-template <typename T, typename Store>
-static pa_status launch_rope_dim(const RopeArgs& a, int32_t head_dim, int32_t num_tokens,
-                                 pa_stream_t stream)
+template <typename T, typename Store, int D>
+static pa_status launch_rope(RopeArgs& a, pa_stream_t stream)
 {
-    return head_dim == 128 ? launch_rope<T, Store, 128>(a, num_tokens, stream)
-                           : launch_rope<T, Store, 64>(a, num_tokens, stream);
+    const int64_t rows = static_cast<int64_t>(a.num_q_heads) + 2 * a.num_kv_heads;
+    const int64_t warps = a.num_tokens * rows * (D / 8) / 32;
+    if (warps >= 4 * kFillWarps) return launch_rope_rows<T, Store, D, 4>(a, stream);
+    if (warps >= 2 * kFillWarps) return launch_rope_rows<T, Store, D, 2>(a, stream);
+    return launch_rope_rows<T, Store, D, 1>(a, stream);
+}
+
+template <typename T, typename Store>
+static pa_status launch_rope_dim(RopeArgs& a, int32_t head_dim, pa_stream_t stream)
+{
+    return head_dim == 128 ? launch_rope<T, Store, 128>(a, stream)
+                           : launch_rope<T, Store, 64>(a, stream);
 }
 
 template <typename T>
-static pa_status launch_rope_store(const RopeArgs& a, pa_dtype pool, int32_t head_dim,
-                                   int32_t num_tokens, pa_stream_t stream)
+static pa_status launch_rope_store(RopeArgs& a, pa_dtype pool, int32_t head_dim, pa_stream_t stream)
 {
     if (pool == PA_DTYPE_FP8_E4M3)
-        return launch_rope_dim<T, E4m3Codes>(a, head_dim, num_tokens, stream);
-    if (pool == PA_DTYPE_INT8) return launch_rope_dim<T, Int8Codes>(a, head_dim, num_tokens, stream);
-    return launch_rope_dim<T, PlainRows>(a, head_dim, num_tokens, stream);
+        return launch_rope_dim<T, E4m3Codes>(a, head_dim, stream);
+    if (pool == PA_DTYPE_INT8) return launch_rope_dim<T, Int8Codes>(a, head_dim, stream);
+    return launch_rope_dim<T, PlainRows>(a, head_dim, stream);
 }
 
 // A token stride in elements: whole 16-byte vectors, at least `need`.
@@ -230,6 +240,7 @@ struct LatentAppendArgs {
     const float* cos_sin;
     const void* weight;
     float eps;
+    uint32_t num_tokens, units;       // units a token
     int32_t num_heads;
     int64_t max_position;
     int32_t interleaved;
@@ -239,19 +250,22 @@ struct LatentAppendArgs {
     int32_t* d_status;
 };
 
-// Grid (token, group of warps).  Warp 0 of a token takes its latent row: L
+// A warp a unit, `units` units a token: unit 0 takes its latent row, L
 // elements over 32 lanes (L / 256 vectors each) and the 64 rotated ones over
-// the first 8 lanes.  Every further warp rotates 4 * STEPS heads of the
-// query, 8 lanes a head, all loads first.
+// the first 8 lanes; every further one rotates 4 * STEPS heads of the query, 8
+// lanes a head, all loads first.
 template <typename T, int L, int STEPS>
 __global__ void __launch_bounds__(kRopeThreads) latent_append_kernel(const LatentAppendArgs a)
 {
     constexpr int VECS = L / 256;
     grid_dependency_wait();
     allow_dependents();
-    const int64_t t = blockIdx.x;
+    const uint32_t item = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t token = item / a.units;
+    if (token >= a.num_tokens) return;
+    const int unit = static_cast<int>(item - token * a.units);
+    const int64_t t = token;
     const int lane = threadIdx.x & 31;
-    const int unit = blockIdx.y * (kRopeThreads / 32) + (threadIdx.x >> 5);
     const int e0 = (lane & 7) * 8;
     const int64_t pos = a.positions[t];
     if (unit == 0) {
@@ -329,29 +343,26 @@ __global__ void __launch_bounds__(kRopeThreads) latent_append_kernel(const Laten
 }
 
 template <typename T, int L, int STEPS>
-static pa_status launch_latent_append(const LatentAppendArgs& a, int32_t num_tokens,
-                                      pa_stream_t stream)
+static pa_status launch_latent_append(LatentAppendArgs& a, pa_stream_t stream)
 {
     constexpr int kWarpsPerCta = kRopeThreads / 32;
     const int64_t units = 1 + (static_cast<int64_t>(a.num_heads) + 4 * STEPS - 1) / (4 * STEPS);
-    const int64_t chunks = (units + kWarpsPerCta - 1) / kWarpsPerCta;
-    if (chunks > 65535) return PA_ERR_UNSUPPORTED;
+    const int64_t items = units * a.num_tokens;
+    if (items > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
+    a.units = static_cast<uint32_t>(units);
     return launch_overlapped(latent_append_kernel<T, L, STEPS>,
-                             dim3(num_tokens, static_cast<unsigned>(chunks)), dim3(kRopeThreads), 0,
-                             stream, a);
+                             dim3(static_cast<unsigned>((items + kWarpsPerCta - 1) / kWarpsPerCta)),
+                             dim3(kRopeThreads), 0, stream, a);
 }
 
 template <typename T>
-static pa_status dispatch_latent_append(const LatentAppendArgs& a, int32_t latent_dim,
-                                        int32_t num_tokens, pa_stream_t stream)
+static pa_status dispatch_latent_append(LatentAppendArgs& a, int32_t latent_dim, pa_stream_t stream)
 {
     // several heads a lane group where the grid fills the GPU without them
-    const bool many = static_cast<int64_t>(num_tokens) * (1 + a.num_heads / 4) >= kFillWarps;
+    const bool many = static_cast<int64_t>(a.num_tokens) * (1 + a.num_heads / 4) >= 4 * kFillWarps;
     if (latent_dim == 512)
-        return many ? launch_latent_append<T, 512, 4>(a, num_tokens, stream)
-                    : launch_latent_append<T, 512, 1>(a, num_tokens, stream);
-    return many ? launch_latent_append<T, 256, 4>(a, num_tokens, stream)
-                : launch_latent_append<T, 256, 1>(a, num_tokens, stream);
+        return many ? launch_latent_append<T, 512, 4>(a, stream) : launch_latent_append<T, 512, 1>(a, stream);
+    return many ? launch_latent_append<T, 256, 4>(a, stream) : launch_latent_append<T, 256, 1>(a, stream);
 }
 
 }  // namespace pa
@@ -416,6 +427,7 @@ extern "C" pa_status pa_rope_append(
     a.q_weight = q_weight;
     a.k_weight = k_weight;
     a.eps = eps;
+    a.num_tokens = static_cast<uint32_t>(num_tokens);
     a.num_q_heads = num_q_heads;
     a.num_kv_heads = num_kv_heads;
     a.rot_dim = rot_dim;
@@ -431,8 +443,8 @@ extern "C" pa_status pa_rope_append(
     a.v_inv = codes && !row_scaled ? 1.0f / v_scale : 1.f;
     a.d_status = d_status;
     return dtype == PA_DTYPE_F16
-               ? launch_rope_store<__half>(a, pool_dtype, head_dim, num_tokens, stream)
-               : launch_rope_store<__nv_bfloat16>(a, pool_dtype, head_dim, num_tokens, stream);
+               ? launch_rope_store<__half>(a, pool_dtype, head_dim, stream)
+               : launch_rope_store<__nv_bfloat16>(a, pool_dtype, head_dim, stream);
 }
 
 extern "C" pa_status pa_latent_append(
@@ -481,6 +493,7 @@ extern "C" pa_status pa_latent_append(
     a.cos_sin = cos_sin;
     a.weight = weight;
     a.eps = eps;
+    a.num_tokens = static_cast<uint32_t>(num_tokens);
     a.num_heads = num_heads;
     a.max_position = max_position;
     a.interleaved = interleaved;
@@ -491,7 +504,6 @@ extern "C" pa_status pa_latent_append(
     a.latent_stride = latent_stride;
     a.num_slots = num_blocks * block_size;
     a.d_status = d_status;
-    return dtype == PA_DTYPE_F16 ? dispatch_latent_append<__half>(a, latent_dim, num_tokens, stream)
-                                 : dispatch_latent_append<__nv_bfloat16>(a, latent_dim, num_tokens,
-                                                                         stream);
+    return dtype == PA_DTYPE_F16 ? dispatch_latent_append<__half>(a, latent_dim, stream)
+                                 : dispatch_latent_append<__nv_bfloat16>(a, latent_dim, stream);
 }
