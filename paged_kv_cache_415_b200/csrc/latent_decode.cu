@@ -35,7 +35,9 @@ static LatentSplit latent_split(int32_t num_seqs, int32_t num_heads, int32_t max
     const int64_t per_seq = (static_cast<int64_t>(max_context_len) + kTile - 1) / kTile;
     s.max_tiles = per_seq * num_seqs;
     const int64_t useful = (s.max_tiles + kMinTiles - 1) / kMinTiles;
-    const int64_t fill = sm_count() / s.groups;
+    // (a combining thread weighs one partial)
+    const int64_t sms = sm_count() < kMaxPartials ? sm_count() : kMaxPartials;
+    const int64_t fill = sms / s.groups;
     s.ctas = static_cast<int32_t>(useful < 1 ? 1 : useful < fill ? useful : fill);
     s.partials = per_seq > 1 && s.ctas > 1;
     return s;
@@ -69,10 +71,10 @@ static pa_status launch_latent_heads(const LatentDecodeArgs& a, const LatentSpli
     // row; else a warp for a row.
     const bool deep = sp.ctas / a.num_seqs >= 2 * kCombineWarps;
     if (deep)
-        return launch_overlapped(latent_combine_kernel<T, L, kCombineWarps>,
+        return launch_overlapped(latent_combine_kernel<T, L, true>,
                                  dim3(static_cast<unsigned>(rows), L / 128), dim3(kCombineWarps * 32),
                                  0, stream, a);
-    return launch_overlapped(latent_combine_kernel<T, L, 1>,
+    return launch_overlapped(latent_combine_kernel<T, L, false>,
                              dim3(static_cast<unsigned>((rows + kCombineWarps - 1) / kCombineWarps)),
                              dim3(kCombineWarps * 32), 0, stream, a);
 }

@@ -18,9 +18,10 @@
 // latent_combine_kernel adds them up in tile order, so results depend on the
 // batch's lengths and the SM count only.
 //
-// Warps: 0-3 softmax and epilogue, 4 copies (TMA, one box of a block and 64
-// columns each), 5 the products for S, 6 those for O^T (apart, so that neither
-// waits in line behind the other).  A stage is filled in parts of 128 columns
+// Warps: 0-3 softmax and epilogue, 4 and 7 copies (TMA, one box of a block and
+// 64 columns each, 50 cycles to issue one: blocks of 16 tokens make 36 a tile,
+// so two warps share a tile's parts), 5 the products for S, 6 those for O^T
+// (apart, so that neither waits in line behind the other).  A stage is filled in parts of 128 columns
 // and S starts with the first that has arrived.
 //
 // Softmax: a thread has two tokens of N / 4 heads.  It keeps a reference m a
@@ -39,7 +40,7 @@
 namespace pa {
 
 constexpr int kTile = 64;                       // tokens of a tile
-constexpr int kLatentThreads = 224;
+constexpr int kLatentThreads = 256;
 constexpr int kMaxGroupHeads = 64;              // heads a CTA serves
 constexpr int kAhead = 3;                       // tiles whose pages are looked up ahead
 constexpr float kRescaleAbove = 8.0f;           // log2 of how far p may pass 1
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     uint64_t* k_full = k_empty + ST;       // [ST][PT]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(k_full + ST * PT);
     int32_t* run = reinterpret_cast<int32_t*>(tmem_slot + 1);     // s0, t0, count
-    int32_t* scan = run + 3;                                      // [7] warp totals
+    int32_t* scan = run + 3;                                      // [8] warp totals
     float* factors = reinterpret_cast<float*>(s_misc + 512);      // [64]
     float* tops = factors + kMaxGroupHeads;                       // [4][64]: of a warp's tokens
 
@@ -260,11 +261,13 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
     const uint32_t leader = elect_lane() ? 1u : 0u;
     bool ok = true;
 
-    if (warp == 4) {
+    if (warp == 4 || warp == 7) {
         // Copies.  Lane l looks up the page of a tile's block l, kAhead tiles in
         // front of the one being copied, so that no copy waits for its table.
+        // Warp 4 takes the even parts and the rotated one, warp 7 the odd ones
+        // and the queries.
+        const bool odd = warp == 7;
         const int block_bytes = a.block_size * 128;       // of one chunk
-        int32_t parts = 0;                                // copied so far
         int32_t it = 0, seg = 0;
         bool fresh = true;                                // first tile of a segment
         int32_t page[kAhead + 1];
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             mk = valid == 64 ? ~0ull : (1ull << valid) - 1;
             const uint32_t bad_blocks = __ballot_sync(kFullMask, bad);
             if (bad_blocks != 0) {
-                if (lane == 0 && group == 0) status_or(a.d_status, PA_STATUS_BAD_BLOCK);
+                if (lane == 0 && group == 0 && !odd) status_or(a.d_status, PA_STATUS_BAD_BLOCK);
                 for (int b = 0; b < blocks; ++b)
                     if (bad_blocks >> b & 1)
                         mk &= ~((a.block_size == 64 ? ~0ull : (1ull << a.block_size) - 1)
@@ -294,6 +297,17 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             }
             ahead.next();
         };
+        auto queries = [&]() {
+            if (leader) {
+                mbar_arrive_expect_tx(q_full, S::kQueryBytes);
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    tma_load_3d(s_query + c * S::kQueryChunk, &tm_query, c * 64,
+                                w.s * a.num_heads + h0, 0, q_full);
+            }
+            ++seg;
+        };
+        if (odd && w.left > 0) queries();                 // the first ones before any rows
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             if (ahead.left > 0) look(page[i], mask[i]);
@@ -305,15 +319,14 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 #pragma unroll
             for (int b = 0; b < 8; ++b) pages[b] = __shfl_sync(kFullMask, page[0], b);
             uint8_t* stage = s_rows + st * S::kStageBytes;
-            // the rotated chunk first: it is free as soon as S is done
+            if (it >= ST) ok = mbar_poll_warp(k_empty + st, (it / ST - 1) & 1);
+            if (!ok) break;
 #pragma unroll
-            for (int i = 0; i < PT; ++i) {
+            for (int i = 0; i < PT; ++i) {                // the rotated chunk first, as S takes it
                 const int p = i == 0 ? PT - 1 : i - 1;
-                const int n = i == 0 ? 1 : 2;                     // chunks
+                const int n = i == 0 ? 1 : 2;             // chunks
+                if ((i > 0 && (p & 1) != 0) != odd) continue;
                 uint64_t* bar = k_full + st * PT + p;
-                if (i == 0 && it >= ST) ok = mbar_poll_warp(k_empty + st, (it / ST - 1) & 1);
-                if (!ok) break;
-                ++parts;
                 if (leader) {
                     // the mask is written before this arrival, its readers wait for it
                     if (i == 0) masks[st] = mask[0];
@@ -328,19 +341,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     }
                 }
             }
-            if (!ok) break;
             ++it;
-            if (fresh) {
-                if (seg > 0) ok = mbar_poll_warp(q_empty, (seg - 1) & 1);
+            if (fresh && it > 1 && odd) {
+                ok = mbar_poll_warp(q_empty, (seg - 1) & 1);
                 if (!ok) break;
-                if (leader) {
-                    mbar_arrive_expect_tx(q_full, S::kQueryBytes);
-#pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        tma_load_3d(s_query + c * S::kQueryChunk, &tm_query, c * 64,
-                                    w.s * a.num_heads + h0, 0, q_full);
-                }
-                ++seg;
+                queries();
             }
             if (ahead.left > 0) look(page[kAhead], mask[kAhead]);
 #pragma unroll
@@ -353,9 +358,11 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         }
         if (!ok) {                                        // let the copies in flight land
             if (lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
-            for (int k = max(0, parts - ST * PT); k < parts; ++k)
-                mbar_poll_warp(k_full + k / PT % ST * PT + (k % PT + PT - 1) % PT, (k / PT / ST) & 1);
-            if (seg > 0) mbar_poll_warp(q_full, (seg - 1) & 1);
+            for (int k = max(0, it - ST); k < it; ++k)
+                for (int p = 0; p < PT; ++p)
+                    if ((p < PT - 1 && (p & 1) != 0) == odd)
+                        mbar_poll_warp(k_full + k % ST * PT + p, (k / ST) & 1);
+            if (odd && seg > 0) mbar_poll_warp(q_full, (seg - 1) & 1);
         }
     } else if (warp == 5) {
         // S^T = R Q^T
@@ -682,52 +689,41 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 
 // Adds up the partials of the sequences that a cut of the work list split:
 // with M = max_p m_p and w_p = 2^(m_p - M),  out = sum w_p O_p / sum w_p l_p,
-// in the order of the CTAs.  With WPR = 1 a warp takes a row of L elements;
-// with eight (few rows of many partials) a CTA takes 128 elements of a row
-// (blockIdx.y) and each warp every eighth partial.
+// in the order of the CTAs.  Where a row has many partials a CTA takes 128
+// elements of one row (DEEP: blockIdx.y), weighs all partials at once and each
+// warp adds up every eighth; else a warp takes a row.
 constexpr int kCombineWarps = 8;
+constexpr int kMaxPartials = 256;                         // of a row: CTAs of the decode kernel
 
-template <typename T, int L, int WPR>
+template <typename T, int L, bool DEEP>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     latent_combine_kernel(const __grid_constant__ LatentDecodeArgs a)
 {
-    grid_dependency_wait();
-    constexpr int PER = WPR == 1 ? L / 128 : 1;           // float4s a lane holds
-    __shared__ float4 s_acc[WPR][WPR == 1 ? 1 : 32];
-    __shared__ float s_sum[kCombineWarps];
+    constexpr int PER = DEEP ? 1 : L / 128;               // float4s a lane holds
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kCombineWarps / WPR) + (WPR == 1 ? warp : 0);
-    if (row >= static_cast<int64_t>(a.num_seqs) * a.num_heads) return;
-    const int s = static_cast<int>(row / a.num_heads), h = static_cast<int>(row % a.num_heads);
+    const int64_t row = DEEP ? static_cast<int64_t>(blockIdx.x)
+                             : static_cast<int64_t>(blockIdx.x) * kCombineWarps + warp;
+    const bool inside = row < static_cast<int64_t>(a.num_seqs) * a.num_heads;
+    const int s = inside ? static_cast<int>(row / a.num_heads) : 0;
+    const int h = inside ? static_cast<int>(row % a.num_heads) : 0;
+    // (the decode kernel has let this launch begin: what it read may be read)
     const int32_t ctx = checked_context(a.context_lens, s, a.max_context_len, a.max_blocks_per_seq,
                                         a.block_size);
-    if (ctx <= 0) return;
+    grid_dependency_wait();
+    if (!inside || ctx <= 0) return;
     const int32_t per_cta = a.ws_meta[0];
     const int32_t begin = a.ws_meta[1 + s];
     const int32_t end = begin + (ctx + kTile - 1) / kTile;
     const int32_t c0 = begin / per_cta, c1 = (end - 1) / per_cta;
     if (c0 == c1) return;                                 // written by the decode kernel
-    const int d0 = WPR == 1 ? 0 : blockIdx.y * 128;
     // A CTA's second slot is its last segment when that is not its first.
     auto slot_of = [&](int32_t c) {
         return (static_cast<int64_t>(c) * 2 + (begin > c * per_cta ? 1 : 0)) * a.num_heads + h;
     };
-    float M = -INFINITY;
-    for (int32_t c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.ws_ml[slot_of(c)].x);
-#pragma unroll
-    for (int k = 16; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, k));
-    const float sub = M == -INFINITY ? 0.f : M;
     float4 acc[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int32_t c = c0 + (WPR == 1 ? 0 : warp); c <= c1; c += WPR) {
-        const int64_t slot = slot_of(c);
-        const float2 ml = a.ws_ml[slot];
-        const float w = exp2f(ml.x - sub);
-        sum = fmaf(w, ml.y, sum);
-        const float4* src = reinterpret_cast<const float4*>(a.ws_o + slot * L + d0) + lane;
+    auto add = [&](float w, const float4* src) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const float4 v = src[i * 32];
@@ -736,25 +732,61 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
             acc[i].z = fmaf(w, v.z, acc[i].z);
             acc[i].w = fmaf(w, v.w, acc[i].w);
         }
-    }
-    if constexpr (WPR > 1) {
+    };
+    float sum = 0.f;
+    if constexpr (DEEP) {
+        __shared__ float s_w[kMaxPartials], s_top[kCombineWarps], s_sum[kCombineWarps];
+        __shared__ float4 s_acc[kCombineWarps][32];
+        const int n = c1 - c0 + 1;                        // at most one a thread
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (static_cast<int>(threadIdx.x) < n) ml = a.ws_ml[slot_of(c0 + threadIdx.x)];
+        float top = ml.x;
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, k));
+        if (lane == 0) s_top[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kCombineWarps; ++i) top = fmaxf(top, s_top[i]);
+        const float w = exp2f(ml.x - (top == -INFINITY ? 0.f : top));
+        s_w[threadIdx.x] = w;
+        float part = w * ml.y;
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) part += __shfl_xor_sync(kFullMask, part, k);
+        if (lane == 0) s_sum[warp] = part;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kCombineWarps; ++i) sum += s_sum[i];
+        const int d0 = blockIdx.y * 128;
+#pragma unroll 8
+        for (int p = warp; p < n; p += kCombineWarps)
+            add(s_w[p], reinterpret_cast<const float4*>(a.ws_o + slot_of(c0 + p) * L + d0) + lane);
         s_acc[warp][lane] = acc[0];
-        if (lane == 0) s_sum[warp] = sum;
         __syncthreads();
         if (warp != 0) return;
         float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-        sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < WPR; ++i) {
+        for (int i = 0; i < kCombineWarps; ++i) {
             const float4 v = s_acc[i][lane];
             r.x += v.x; r.y += v.y; r.z += v.z; r.w += v.w;
-            sum += s_sum[i];
         }
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * L + d0 + lane * 4) =
             make_uint2(Elem<T>::from_float2(r.x * inv, r.y * inv),
                        Elem<T>::from_float2(r.z * inv, r.w * inv));
     } else {
+        float top = -INFINITY;
+        for (int32_t c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, a.ws_ml[slot_of(c)].x);
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, k));
+        const float sub = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+        for (int32_t c = c0; c <= c1; ++c) {
+            const int64_t slot = slot_of(c);
+            const float2 ml = a.ws_ml[slot];
+            const float w = exp2f(ml.x - sub);
+            sum = fmaf(w, ml.y, sum);
+            add(w, reinterpret_cast<const float4*>(a.ws_o + slot * L) + lane);
+        }
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
