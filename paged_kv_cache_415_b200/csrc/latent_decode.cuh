@@ -270,31 +270,15 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         const int block_bytes = a.block_size * 128;       // of one chunk
         int32_t it = 0, seg = 0;
         bool fresh = true;                                // first tile of a segment
-        int32_t page[kAhead + 1];
-        uint64_t mask[kAhead + 1];
+        int32_t page[kAhead + 1];                         // as the table has them
         TileWalk ahead = w;
-        auto look = [&](int32_t& pg, uint64_t& mk) {
+        auto look = [&](int32_t& pg) {
             const int32_t t0 = ahead.tile * kTile;
-            const int32_t valid = min(kTile, ahead.ctx - t0);
-            const int blocks = (valid + a.block_size - 1) / a.block_size;
+            const int32_t blocks = (min(kTile, ahead.ctx - t0) + a.block_size - 1) / a.block_size;
             pg = 0;
-            bool bad = false;
-            if (lane < blocks) {
+            if (lane < blocks)
                 pg = a.block_tables[static_cast<int64_t>(ahead.s) * a.max_blocks_per_seq +
                                     t0 / a.block_size + lane];
-                bad = pg < 0 || pg >= a.num_blocks;
-                // a block outside the pool reads as zeros, beyond the map's end
-                if (bad) pg = static_cast<int32_t>(a.num_blocks);
-            }
-            mk = valid == 64 ? ~0ull : (1ull << valid) - 1;
-            const uint32_t bad_blocks = __ballot_sync(kFullMask, bad);
-            if (bad_blocks != 0) {
-                if (lane == 0 && group == 0 && !odd) status_or(a.d_status, PA_STATUS_BAD_BLOCK);
-                for (int b = 0; b < blocks; ++b)
-                    if (bad_blocks >> b & 1)
-                        mk &= ~((a.block_size == 64 ? ~0ull : (1ull << a.block_size) - 1)
-                                << (b * a.block_size));
-            }
             ahead.next();
         };
         auto queries = [&]() {
@@ -310,14 +294,27 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
         if (odd && w.left > 0) queries();                 // the first ones before any rows
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (ahead.left > 0) look(page[i], mask[i]);
+            if (ahead.left > 0) look(page[i]);
         while (w.left > 0 && ok) {
             const int st = it % ST;
             const int32_t valid = min(kTile, w.ctx - w.tile * kTile);
             const int blocks = (valid + a.block_size - 1) / a.block_size;
+            if (ahead.left > 0) look(page[kAhead]);
+            uint64_t mask = valid == 64 ? ~0ull : (1ull << valid) - 1;
+            const bool bad = lane < blocks && (page[0] < 0 || page[0] >= a.num_blocks);
+            // a block outside the pool reads as zeros, beyond the map's end
+            const int32_t mine = bad ? static_cast<int32_t>(a.num_blocks) : page[0];
+            const uint32_t bad_blocks = __ballot_sync(kFullMask, bad);
+            if (bad_blocks != 0) {
+                if (lane == 0 && group == 0 && !odd) status_or(a.d_status, PA_STATUS_BAD_BLOCK);
+                for (int b = 0; b < blocks; ++b)
+                    if (bad_blocks >> b & 1)
+                        mask &= ~((a.block_size == 64 ? ~0ull : (1ull << a.block_size) - 1)
+                                  << (b * a.block_size));
+            }
             int32_t pages[8];
 #pragma unroll
-            for (int b = 0; b < 8; ++b) pages[b] = __shfl_sync(kFullMask, page[0], b);
+            for (int b = 0; b < 8; ++b) pages[b] = __shfl_sync(kFullMask, mine, b);
             uint8_t* stage = s_rows + st * S::kStageBytes;
             if (it >= ST) ok = mbar_poll_warp(k_empty + st, (it / ST - 1) & 1);
             if (!ok) break;
@@ -329,7 +326,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 uint64_t* bar = k_full + st * PT + p;
                 if (leader) {
                     // the mask is written before this arrival, its readers wait for it
-                    if (i == 0) masks[st] = mask[0];
+                    if (i == 0) masks[st] = mask;
                     mbar_arrive_expect_tx(bar, blocks * block_bytes * n);
 #pragma unroll
                     for (int b = 0; b < 8; ++b) {
@@ -347,12 +344,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 if (!ok) break;
                 queries();
             }
-            if (ahead.left > 0) look(page[kAhead], mask[kAhead]);
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                page[i] = page[i + 1];
-                mask[i] = mask[i + 1];
-            }
+            for (int i = 0; i < kAhead; ++i) page[i] = page[i + 1];
             fresh = w.last();
             w.next();
         }
@@ -496,6 +489,27 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             // looked at early, used where P^T is written
             const bool pv_ready = it == 0 || mbar_test(pv_done, (it - 1) & 1);
             const bool on[2] = {(mask >> tok & 1) != 0, (mask >> (tok + 8) & 1) != 0};
+            if (fresh && mask != 0) {
+                // The segment's references: the scores of its first token that
+                // counts.  (Its maxima would do as well, for three shuffles and
+                // an exchange more a head: p may pass 1 by 2^8.)
+                const int f = __ffsll(static_cast<long long>(mask)) - 1;
+                if ((tok & ~8) == (f & ~8)) {
+                    const int half = f >> 3 & 1;
+#pragma unroll
+                    for (int k = 0; k < J; ++k)
+                        *reinterpret_cast<float2*>(tops + 8 * k + head0) = make_float2(
+                            __uint_as_float(half ? x[4 * k + 2] : x[4 * k]) * a.scale_log2,
+                            __uint_as_float(half ? x[4 * k + 3] : x[4 * k + 1]) * a.scale_log2);
+                }
+                named_barrier(1, 128);
+#pragma unroll
+                for (int k = 0; k < J; ++k) {
+                    const float2 v = *reinterpret_cast<const float2*>(tops + 8 * k + head0);
+                    if (8 * k + head0 < heads) m[2 * k] = v.x;
+                    if (8 * k + head0 + 1 < heads) m[2 * k + 1] = v.y;
+                }
+            }
             float y[4 * J];
             auto shift = [&]() {                          // y = log2 of the weights
 #pragma unroll
@@ -638,37 +652,46 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                 wait(pv_done, it & 1);
                 tmem_fence_after();
                 uint8_t* mine = s_p + warp * 1024;        // P^T has been used
+                // two groups of 16 columns at a time
 #pragma unroll 1
-                for (int c = 0; c < NB * N; c += 16) {
-                    const int n0 = c % N, d0 = c / N * 128 + warp * 32;
-                    if (n0 >= heads) continue;
-                    uint32_t o[16];
-                    tmem_ld16(o, lanes + S::kOCol + c);
+                for (int c2 = 0; c2 < NB * N; c2 += 32) {
+                    uint32_t o[2][16];
+                    tmem_ld16(o[0], lanes + S::kOCol + c2);
+                    tmem_ld16(o[1], lanes + S::kOCol + c2 + 16);
                     tmem_wait_ld();
-                    if (split) {
-                        float* dst = a.ws_o + (slot * a.num_heads + h0 + n0) * L + d0 + lane;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (n0 + i < heads) dst[i * L] = __uint_as_float(o[i]);
-                    } else {
-                        // through shared memory: 16 heads x 32 elements, then 16 bytes a lane
-                        float fc[16];
-                        load16(fc, factors + n0);
+                    for (int q = 0; q < 2; ++q) {
+                        const int c = c2 + 16 * q;
+                        const int n0 = c % N, d0 = c / N * 128 + warp * 32;
+                        const int left = heads - n0;      // heads of this group
+                        if (left <= 0) continue;
+                        if (split) {
+                            float* dst = a.ws_o + (slot * a.num_heads + h0 + n0) * L + d0 + lane;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            reinterpret_cast<T*>(mine)[i * 32 + lane] = T(__uint_as_float(o[i]) * fc[i]);
-                        __syncwarp();
+                            for (int i = 0; i < 16; ++i)
+                                if (i < left) dst[i * L] = __uint_as_float(o[q][i]);
+                        } else {
+                            // through shared memory: 16 heads x 32 elements, then 16 bytes a lane
+                            float fc[16];
+                            load16(fc, factors + n0);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int i = k * 8 + (lane >> 2);
-                            const uint4 v = *reinterpret_cast<const uint4*>(mine + i * 64 + (lane & 3) * 16);
-                            if (n0 + i < heads)
-                                *reinterpret_cast<uint4*>(
-                                    static_cast<T*>(a.out) +
-                                    (static_cast<int64_t>(w.s) * a.num_heads + h0 + n0 + i) * L + d0 +
-                                    (lane & 3) * 8) = v;
+                            for (int i = 0; i < 16; ++i)
+                                reinterpret_cast<T*>(mine)[i * 32 + lane] =
+                                    T(__uint_as_float(o[q][i]) * fc[i]);
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int i = k * 8 + (lane >> 2);
+                                const uint4 v =
+                                    *reinterpret_cast<const uint4*>(mine + i * 64 + (lane & 3) * 16);
+                                if (i < left)
+                                    *reinterpret_cast<uint4*>(
+                                        static_cast<T*>(a.out) +
+                                        (static_cast<int64_t>(w.s) * a.num_heads + h0 + n0 + i) * L + d0 +
+                                        (lane & 3) * 8) = v;
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
                     }
                 }
                 tmem_fence_before();
