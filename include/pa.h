@@ -639,6 +639,8 @@ PA_API pa_status pa_paged_decode_no_alloc(void* out, const void* query, const vo
  *                many sines.  16-byte aligned; may be NULL if rot_dim is 0.
  * q_weight, k_weight  [D] of `dtype`, or NULL.  eps finite, not negative.
  * rot_dim        0 .. D, a multiple of 16 (else PA_ERR_UNSUPPORTED).
+ * num_tokens     0: nothing is done, and the tensors' pointers may be NULL (so
+ *                in the calls on latent pools, also with num_seqs 0).
  * d_status       optional; PA_STATUS_BAD_SLOT (the queries are still
  *                written), PA_STATUS_BAD_POSITION.
  */
@@ -726,6 +728,8 @@ PA_API pa_status pa_latent_decode(void* out, const void* query, const void* cach
  * tokens at positions up to context_lens[s] - n + i:
  *   x_t = scale * (q_nope . K_nope_t + q_rope . r_t),
  *   out = sum_t softmax(x)_t V_t.
+ * A query that sees a token of which some element of V (rounded to 16 bits) is
+ * not finite gives NaN in that head; queries before the token do not meet it.
  *
  * out            [num_tokens][num_heads][value_dim], 16-byte aligned; written
  *                for the rows of the sequences, others are left as they were.

@@ -2,9 +2,11 @@
 
 The product is the C-ABI library ``libpa.so`` (declared in include/pa.h):
 ``pa_reshape_and_cache``, ``pa_copy_blocks`` and ``pa_paged_decode`` (plus
-``pa_paged_decode_no_alloc``), all hand-written CUDA.  ``binding`` wraps them
-for torch CUDA tensors (argument marshalling only); ``step`` strings the
-calls into one decode step; ``build`` compiles the library.
+``pa_paged_decode_no_alloc``), the rotating appends and attention over latent
+pools (``pa_rope_append``, ``pa_latent_append``, ``pa_latent_decode``,
+``pa_latent_prefill``), all hand-written CUDA.  ``binding`` wraps them for
+torch CUDA tensors (argument marshalling only); ``step`` strings the calls
+into one decode step; ``build`` compiles the library.
 
 The binding is loaded on first use of any of its names and raises if
 libpa.so has not been built: there is no fallback.

@@ -101,7 +101,7 @@ extern "C" size_t pa_latent_decode_workspace_size(int32_t num_seqs, int32_t num_
     using namespace pa;
     if (bad_latent_shape(num_seqs, num_heads, latent_dim, block_size, max_context_len) ||
         !supported_latent(latent_dim, 64) || !supported_latent_block(block_size) ||
-        num_heads > kMaxLatentHeads)
+        num_heads > kMaxLatentHeads || num_seqs > 65535)
         return 0;
     const LatentSplit sp = latent_split(num_seqs, num_heads, max_context_len);
     if (!sp.partials) return 0;
@@ -125,6 +125,7 @@ extern "C" pa_status pa_latent_decode(void* out, const void* query, const void* 
     if (!supported_dtype(dtype) || !supported_latent(latent_dim, rope_dim) ||
         !supported_latent_block(block_size) || num_heads > kMaxLatentHeads || num_seqs > 65535)
         return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
     if (!out || !query || !cache || !block_tables || !context_lens) return PA_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(query) || !aligned16(cache) || !aligned4(block_tables) ||
         !aligned4(context_lens) || (d_status && !aligned4(d_status)))
@@ -133,9 +134,8 @@ extern "C" pa_status pa_latent_decode(void* out, const void* query, const void* 
                                                         max_context_len);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
         return PA_ERR_INVALID_ARG;
-    if (num_seqs == 0) return PA_OK;
     const LatentSplit sp = latent_split(num_seqs, num_heads, max_context_len);
-    if (sp.max_tiles > (1 << 30) || num_blocks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
+    if (sp.max_tiles > (1 << 30) || max_context_len > 0x7fffffff - kTile || num_blocks > 0x7fffffff) return PA_ERR_UNSUPPORTED;
     LatentDecodeArgs a = {};
     a.out = out;
     a.block_tables = block_tables;

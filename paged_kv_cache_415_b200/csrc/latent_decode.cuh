@@ -31,6 +31,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -492,7 +493,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             if (fresh && mask != 0) {
                 // The segment's references: the scores of its first token that
                 // counts.  (Its maxima would do as well, for three shuffles and
-                // an exchange more a head: p may pass 1 by 2^8.)
+                // an exchange more a head: p may pass 1 by 2^8.)  Not below the
+                // least finite value: a score of -inf less itself would be NaN.
                 const int f = __ffsll(static_cast<long long>(mask)) - 1;
                 if ((tok & ~8) == (f & ~8)) {
                     const int half = f >> 3 & 1;
@@ -506,8 +508,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 #pragma unroll
                 for (int k = 0; k < J; ++k) {
                     const float2 v = *reinterpret_cast<const float2*>(tops + 8 * k + head0);
-                    if (8 * k + head0 < heads) m[2 * k] = v.x;
-                    if (8 * k + head0 + 1 < heads) m[2 * k + 1] = v.y;
+                    if (8 * k + head0 < heads) m[2 * k] = fmaxf(v.x, -FLT_MAX);
+                    if (8 * k + head0 + 1 < heads) m[2 * k + 1] = fmaxf(v.y, -FLT_MAX);
                 }
             }
             float y[4 * J];

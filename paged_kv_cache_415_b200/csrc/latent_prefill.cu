@@ -15,12 +15,12 @@
 
 namespace pa {
 
-// The workspace: K and V of every head, the rotated part, one mask bit a
-// token; a sequence's rows are whole tiles of keys.
+// The workspace: K and V of every head, the rotated part, one mask bit a token
+// and one a token and head; a sequence's rows are whole tiles of keys.
 struct PrefillSpace {
     int64_t rows;
-    size_t key_bytes, rot_bytes, mask_bytes;
-    size_t total() const { return 2 * key_bytes + rot_bytes + mask_bytes; }
+    size_t key_bytes, rot_bytes, mask_bytes, odd_bytes;
+    size_t total() const { return 2 * key_bytes + rot_bytes + mask_bytes + odd_bytes; }
 };
 
 static PrefillSpace prefill_space(int32_t num_seqs, int32_t num_heads, int32_t max_context_len)
@@ -31,6 +31,7 @@ static PrefillSpace prefill_space(int32_t num_seqs, int32_t num_heads, int32_t m
     s.key_bytes = all * num_heads * kNope * 2;
     s.rot_bytes = all * kRot * 2;
     s.mask_bytes = all / 8;
+    s.odd_bytes = all * num_heads / 8;
     return s;
 }
 
@@ -101,7 +102,7 @@ extern "C" size_t pa_latent_prefill_workspace_size(int32_t num_seqs, int32_t num
     using namespace pa;
     if (bad_latent_shape(num_seqs, num_heads, latent_dim, block_size, max_context_len) ||
         !supported_latent(latent_dim, 64) || !supported_latent_block(block_size) ||
-        num_heads > kMaxLatentHeads)
+        num_heads > kMaxLatentHeads || num_seqs > 65535)
         return 0;
     return prefill_space(num_seqs, num_heads, max_context_len).total();
 }
@@ -123,6 +124,7 @@ extern "C" pa_status pa_latent_prefill(
         value_dim != kValue || !supported_latent_block(block_size) || num_heads > kMaxLatentHeads ||
         num_seqs > 65535)
         return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
     if (!out || !query || !cache || !w_kv || !block_tables || !query_starts || !context_lens)
         return PA_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(query) || !aligned16(cache) || !aligned16(w_kv) ||
@@ -133,7 +135,6 @@ extern "C" pa_status pa_latent_prefill(
                                                          block_size, max_context_len);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
         return PA_ERR_INVALID_ARG;
-    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
     const PrefillSpace sp = prefill_space(num_seqs, num_heads, max_context_len);
     if (sp.rows > 65535LL * kKvTile || num_blocks > 0x7fffffff ||
         max_query_len > 65535LL * 2 * kQueryTile)
@@ -149,6 +150,7 @@ extern "C" pa_status pa_latent_prefill(
     a.ws_v = ws + sp.key_bytes;
     a.ws_rot = ws + 2 * sp.key_bytes;
     a.ws_mask = reinterpret_cast<uint32_t*>(ws + 2 * sp.key_bytes + sp.rot_bytes);
+    a.ws_odd = reinterpret_cast<uint32_t*>(ws + 2 * sp.key_bytes + sp.rot_bytes + sp.mask_bytes);
     a.rows = static_cast<int32_t>(sp.rows);
     a.num_seqs = num_seqs;
     a.num_tokens = num_tokens;

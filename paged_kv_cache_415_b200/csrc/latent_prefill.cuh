@@ -19,6 +19,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "pa_common.cuh"
 #include "tcgen05.cuh"
 
@@ -40,6 +42,7 @@ struct LatentPrefillArgs {
     void* ws_v;                 // [S][H][rows][128]
     void* ws_rot;               // [S][rows][64]
     uint32_t* ws_mask;          // [S][rows / 32]: tokens that count
+    uint32_t* ws_odd;           // [S][H][rows / 32]: tokens whose value is not finite
     int32_t rows;               // max_context_len rounded up to whole tiles
     int32_t num_seqs, num_tokens, num_heads, heads_per_cta, block_size, max_blocks_per_seq;
     int64_t num_blocks;
@@ -86,6 +89,19 @@ struct ExpandShape {
 };
 
 constexpr int kExpandThreads = 192;
+
+// z + 0 p on pairs: a z that begins at 0 stays 0 unless some element of some p
+// is not finite.
+template <typename T>
+__device__ __forceinline__ uint32_t add_times_zero(uint32_t p, uint32_t z)
+{
+    uint32_t d;
+    if constexpr (std::is_same<T, __half>::value)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(p), "r"(0u), "r"(z));
+    else
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(p), "r"(0u), "r"(z));
+    return d;
+}
 
 // Grid (group of heads, tile of 128 tokens, sequence).  Warps: 0-3 store, 4
 // copies, 5 products; two accumulators of 256 columns (key, value) alternate.
@@ -245,6 +261,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         for (int h = 0; h < heads; ++h) {
             const int b = h & 1;
+            uint32_t odd = 0;                             // not 0: some element of V is not finite
             // a wait that gave up is not repeated: the warps walk on together, so
             // that none is left alone at a barrier (PA_STATUS_TIMEOUT)
             if (ok) ok = mbar_poll_warp(o_full + b, (h / 2) & 1);
@@ -259,21 +276,35 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                     tmem_fence_before();
                     mbar_arrive(o_empty + b);
                 }
+                // A token that does not count is a row of zeros: 0 times what its
+                // place holds may not be 0.  So is a value that is not finite: a
+                // query before its token must not meet it, those that see it take
+                // it from ws_odd.
+                uint32_t p[8][4];
+                uint32_t trace = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    p[i >> 2][i & 3] = Elem<T>::from_float2(__uint_as_float(o[i >> 4][2 * i & 31]),
+                                                            __uint_as_float(o[i >> 4][(2 * i & 31) + 1]));
+                    trace = add_times_zero<T>(p[i >> 2][i & 3], trace);
+                }
+                bool keep = counts;
+                if (c >= 2) {
+                    odd |= trace;
+                    keep = keep && trace == 0;
+                }
+                if (c == 3) {
+                    const uint32_t word = __ballot_sync(kFullMask, counts && odd != 0);
+                    if (lane == 0)
+                        a.ws_odd[((static_cast<int64_t>(s) * a.num_heads + h0 + h) * a.rows + t) >> 5] = word;
+                }
                 // the last box has been read out of shared memory
                 if (r == 0) tma_store_wait_read<0>();
                 named_barrier(1, 128);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t p[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        p[e] = Elem<T>::from_float2(__uint_as_float(o[i >> 2][8 * (i & 3) + 2 * e]),
-                                                    __uint_as_float(o[i >> 2][8 * (i & 3) + 2 * e + 1]));
-                    // a token that does not count is a row of zeros: 0 times what
-                    // its place holds may not be 0
+                for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<uint4*>(s_out + r * 128 + ((i ^ (r & 7)) << 4)) =
-                        counts ? make_uint4(p[0], p[1], p[2], p[3]) : make_uint4(0, 0, 0, 0);
-                }
+                        keep ? make_uint4(p[i][0], p[i][1], p[i][2], p[i][3]) : make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
                 named_barrier(1, 128);
                 if (r == 0) {
@@ -531,6 +562,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const uint32_t s_tmem = tmem + quarter + t * kKvTile;
         const uint32_t o_tmem = tmem + quarter + S::kOCol + t * kValue;
         grid_dependency_wait();                           // the masks are the expansion's
+        const uint32_t* odd_words = a.ws_odd + ((static_cast<int64_t>(s) * a.num_heads + h) * a.rows >> 5);
+        uint32_t any_odd = 0;
+        for (int32_t i = lane; i < n; i += 32) {
+            const uint4 v = reinterpret_cast<const uint4*>(odd_words)[i];
+            any_odd |= v.x | v.y | v.z | v.w;
+        }
+        const bool odd = __any_sync(kFullMask, any_odd != 0);
         float m = -INFINITY, l = 0.f;
         for (int32_t i = 0; i < n; ++i) {
             const int32_t t0 = i * kKvTile;
@@ -600,6 +638,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 tmem_st32(s_tmem + 32 * c, p);
             }
             l += sum.x + sum.y;
+            if (odd) {                                    // a value that is not finite makes NaN
+                for (int k = 0; k < kKvTile / 32; ++k) {
+                    const int32_t ends = last - t0 - 32 * k;      // the last token seen of this word
+                    const uint32_t sees = ends >= 31 ? ~0u : ends < 0 ? 0u : (2u << ends) - 1;
+                    if (odd_words[t0 / 32 + k] & sees) l = NAN;
+                }
+            }
             tmem_wait_st();
             tmem_fence_before();
             mbar_arrive(p_full + t);
@@ -608,7 +653,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         if (ok && n > 0) ok = mbar_poll_warp(pv_done + t, (n - 1) & 1);
         if (ok && n > 0) {
             tmem_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             // Through shared memory (the tile's queries have been used), 8 KB a
             // warp: stored a row a thread, the 32 lines that each store touches
             // took 9000 cycles.  16-byte chunk j of row r lies at j ^ (r % 8).

@@ -395,6 +395,7 @@ extern "C" pa_status pa_rope_append(
     if (codes && !row_scaled &&
         (!(k_scale > 0.f) || !(v_scale > 0.f) || !isfinite(k_scale) || !isfinite(v_scale)))
         return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
     if (!query_out || !query || !key || !value || !k_cache || !v_cache || !slot_mapping ||
         !positions || (rot_dim > 0 && !cos_sin))
         return PA_ERR_INVALID_ARG;
@@ -411,7 +412,6 @@ extern "C" pa_status pa_rope_append(
         !good_stride(key_stride, kv_row, num_tokens) ||
         !good_stride(value_stride, kv_row, num_tokens))
         return PA_ERR_INVALID_ARG;
-    if (num_tokens == 0) return PA_OK;
     RopeArgs a;
     a.query_out = query_out;
     a.query = query;
@@ -464,6 +464,7 @@ extern "C" pa_status pa_latent_append(
         !supported_latent_block(block_size))
         return PA_ERR_UNSUPPORTED;
     if (!(eps >= 0.f) || !isfinite(eps)) return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
     if (!latent || !cache || !slot_mapping || !positions || !cos_sin ||
         (num_heads > 0 && (!query_out || !query_rope)))
         return PA_ERR_INVALID_ARG;
@@ -482,7 +483,6 @@ extern "C" pa_status pa_latent_append(
             !good_stride(query_stride, in_row, num_tokens))
             return PA_ERR_INVALID_ARG;
     }
-    if (num_tokens == 0) return PA_OK;
     LatentAppendArgs a;
     a.query_out = query_out;
     a.query_rope = query_rope;

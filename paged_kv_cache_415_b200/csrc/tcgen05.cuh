@@ -355,17 +355,7 @@ __device__ __forceinline__ void prefetch_tensor_map(const void* tensor_map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tensor_map)) : "memory");
 }
 
-// Tiled tensor copy global -> shared of one box of a 2-D / 3-D tensor map.
-__device__ __forceinline__ void tma_load_2d(void* dst_smem, const void* tensor_map, int x, int y,
-                                            uint64_t* bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst_smem)),
-        "l"(reinterpret_cast<uint64_t>(tensor_map)), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-
+// Tiled tensor copy global -> shared of one box of a 3-D tensor map.
 __device__ __forceinline__ void tma_load_3d(void* dst_smem, const void* tensor_map, int x, int y,
                                             int z, uint64_t* bar)
 {

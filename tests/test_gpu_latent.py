@@ -3,8 +3,8 @@ and a prompt followed by decode steps as a model runs them."""
 import pytest
 import torch
 
-from tests.latent_reference import (F64, angle_table, assert_within, attend, half_step,
-                                    latent_decode, latent_prefill, normed, rotated)
+from tests.latent_reference import (F64, angle_table, assert_within, attend, context_rows,
+                                    half_step, latent_decode, latent_prefill, normed, rotated)
 
 pytestmark = pytest.mark.gpu
 BAD_BLOCK, BAD_CONTEXT = 1, 4
@@ -393,3 +393,96 @@ def test_attend_bound_is_tight_enough_to_fail():
     wrong, _ = attend(q, rows, rows[:, :256], seen, 0.05, torch.float16)
     with pytest.raises(AssertionError):
         assert_within(wrong, ref, bound, "planted")
+
+
+# ---------------------------------------------------------------------------
+# Wide groups, nothing to do, values that are not finite
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("heads,lat", [(64, 256), (128, 256), (48, 512), (17, 256)])
+def test_decode_group_widths(heads, lat):
+    g = torch.Generator().manual_seed(heads + lat)
+    context = [333, 64, 2, 1025]
+    cache, tables = _pool(context, 16, lat, torch.bfloat16, g)
+    query = torch.randn(len(context), heads, lat + 64, generator=g).to(torch.bfloat16)
+    ctx = torch.tensor(context, dtype=torch.int32)
+    out = _decode(query, cache, tables, ctx, 0.05)
+    ref, bound = latent_decode(query, cache, tables, ctx, 0.05)
+    assert_within(out.cpu(), ref, bound, "decode")
+
+
+def test_nothing_to_do():
+    """Empty contexts alone, no sequences, no new tokens."""
+    from paged_kv_cache_415_b200 import binding as B
+    g = torch.Generator().manual_seed(9)
+    cache, tables = _pool([0, 0, 0], 16, 512, torch.float16, g)
+    query = torch.randn(3, 20, 576, generator=g).to(torch.float16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    empty = torch.zeros(3, dtype=torch.int32)
+    assert B.pa_latent_decode_workspace_size(3, 20, 512, 16, 0) == 0
+    assert (_decode(query, cache, tables, empty, 0.1, max_context=0, status=status) == 0).all()
+    assert (_decode(query, cache, tables, empty, 0.1, max_context=900, status=status) == 0).all()
+    assert _decode(query[:0], cache, tables[:0], empty[:0], 0.1, max_context=64).shape[0] == 0
+    q = torch.randn(4, 2, 192, generator=g).to(torch.float16)
+    w = torch.randn(2, 256, 512, generator=g).to(torch.float16)
+    starts = torch.zeros(4, dtype=torch.int32)
+    out = _prefill(q, cache, w, tables, starts, empty, 0.1, max_new=4, max_context=16,
+                   status=status)
+    assert (out == 9).all()
+    out = _prefill(q, cache, w, tables, starts, empty, 0.1, max_new=0, max_context=0, status=status)
+    assert (out == 9).all() and int(status) == 0
+
+
+@pytest.mark.parametrize("masked", [1, 64, 100, 200])
+def test_decode_scores_of_minus_infinity(masked):
+    """The first `masked` tokens score minus infinity (through their rotated
+    part): they weigh nothing, whichever tile the first finite score is in."""
+    g = torch.Generator().manual_seed(masked)
+    cache, tables = _pool([300], 16, 256, torch.bfloat16, g)
+    query = torch.randn(1, 16, 320, generator=g).to(torch.bfloat16)
+    query[..., 256] = query[..., 256].abs() + 0.5
+    t = torch.arange(masked)
+    cache[tables[0][t // 16].long(), t % 16, 256] = 0
+    ctx = torch.tensor([300], dtype=torch.int32)
+    rows, _ = context_rows(cache, tables[0], 300)
+    seen = (torch.arange(300) >= masked).expand(16, 300)
+    ref, bound = attend(query[0].to(F64), rows, rows[:, :256], seen, 0.05, torch.bfloat16)
+    cache[tables[0][t // 16].long(), t % 16, 256] = -float("inf")
+    out = _decode(query, cache, tables, ctx, 0.05)
+    assert_within(out.cpu()[0], ref, bound, "decode")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("worst", [float("inf"), float("nan")])
+def test_prefill_later_tokens_do_not_reach_back(dtype, worst):
+    """Tokens that are not finite: queries before them are what they are
+    without them, those that see them are not finite."""
+    x = _prompt(3, 256, 16, [200, 90], [100, 0], dtype, 21)
+    query, cache, w, tables, starts, ctx = x
+    first = {0: 250, 1: 40}                            # of the new ones, 150 and 40
+    for s, t in first.items():
+        cache[tables[s, t // 16], t % 16] = 0
+        cache[tables[s, (t + 9) // 16], (t + 9) % 16] = 0
+    ref, bound = latent_prefill(*x, 0.07)
+    for s, t in first.items():
+        cache[tables[s, t // 16], t % 16, :256] = worst
+        cache[tables[s, (t + 9) // 16], (t + 9) % 16, 7] = worst
+    out = _prefill(*x, 0.07).cpu()
+    for rows in (slice(0, 150), slice(200, 240)):
+        assert_within(out[rows], ref[rows], bound[rows], "before")
+    for rows in (slice(150, 200), slice(240, 290)):
+        assert not torch.isfinite(out[rows]).all(-1).any()
+
+
+def test_prefill_value_past_the_type():
+    """A value of one head past the type's range: that head's queries alone."""
+    x = _prompt(2, 512, 32, [60], [40], torch.float16, 22)
+    query, cache, w, tables, starts, ctx = x
+    # head 0's value element 5 of token 20 is about 300 * 512 * 0.8, of others 300 * 512^0.5
+    w[0, 128 + 5] = torch.where(cache[tables[0, 0], 20, :512] < 0, -300.0, 300.0).half()
+    out = _prefill(*x, 0.07).cpu()
+    assert torch.isnan(out[:, 0]).all()
+    safe = w.clone()
+    safe[0] = 0
+    ref, bound = latent_prefill(query, cache, safe, tables, starts, ctx, 0.07)
+    assert_within(out[:, 1], ref[:, 1], bound[:, 1], "other head")

@@ -186,3 +186,22 @@ def test_binding_checks_what_the_library_cannot_see(pa):
             pa.pa_latent_decode(**{**good, name: value})
     with pytest.raises(ValueError, match="CUDA"):
         pa.pa_latent_decode(**good)
+
+
+def test_empty_calls_take_null_tensors(pa):
+    """Tensors of no elements have no address."""
+    none = dict.fromkeys(("query_out", "query", "key", "value", "slot_mapping", "positions"))
+    assert _rope(pa, num_tokens=0, **none) == OK
+    none = dict.fromkeys(("query_out", "query_rope", "latent", "slot_mapping", "positions"))
+    assert _append(pa, num_tokens=0, **none) == OK
+    none = dict.fromkeys(("out", "query", "block_tables", "context_lens", "workspace"))
+    assert _decode(pa, num_seqs=0, **none) == OK
+    assert _prefill(pa, num_seqs=0, **none) == OK
+    assert _prefill(pa, num_tokens=0, out=None, query=None) == OK
+
+
+def test_sizes_past_the_limits(pa):
+    assert pa.LIB.pa_latent_decode_workspace_size(65536, 16, 512, 16, 4096) == 0
+    assert pa.LIB.pa_latent_prefill_workspace_size(65536, 16, 512, 16, 4096) == 0
+    assert _decode(pa, num_seqs=65536) == UNSUPPORTED
+    assert _prefill(pa, num_seqs=65536) == UNSUPPORTED
