@@ -15,12 +15,12 @@
 
 namespace pa {
 
-// The workspace: K and V of every head, the rotated part, one mask bit a token
-// and one a token and head; a sequence's rows are whole tiles of keys.
+// The workspace: K and V of every head, the rotated part, one mask bit a
+// token; a sequence's rows are whole tiles of keys.
 struct PrefillSpace {
     int64_t rows;
-    size_t key_bytes, rot_bytes, mask_bytes, odd_bytes;
-    size_t total() const { return 2 * key_bytes + rot_bytes + mask_bytes + odd_bytes; }
+    size_t key_bytes, rot_bytes, mask_bytes;
+    size_t total() const { return 2 * key_bytes + rot_bytes + mask_bytes; }
 };
 
 static PrefillSpace prefill_space(int32_t num_seqs, int32_t num_heads, int32_t max_context_len)
@@ -31,7 +31,6 @@ static PrefillSpace prefill_space(int32_t num_seqs, int32_t num_heads, int32_t m
     s.key_bytes = all * num_heads * kNope * 2;
     s.rot_bytes = all * kRot * 2;
     s.mask_bytes = all / 8;
-    s.odd_bytes = all * num_heads / 8;
     return s;
 }
 
@@ -150,7 +149,6 @@ extern "C" pa_status pa_latent_prefill(
     a.ws_v = ws + sp.key_bytes;
     a.ws_rot = ws + 2 * sp.key_bytes;
     a.ws_mask = reinterpret_cast<uint32_t*>(ws + 2 * sp.key_bytes + sp.rot_bytes);
-    a.ws_odd = reinterpret_cast<uint32_t*>(ws + 2 * sp.key_bytes + sp.rot_bytes + sp.mask_bytes);
     a.rows = static_cast<int32_t>(sp.rows);
     a.num_seqs = num_seqs;
     a.num_tokens = num_tokens;

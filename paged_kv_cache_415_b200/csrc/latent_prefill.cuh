@@ -42,7 +42,6 @@ struct LatentPrefillArgs {
     void* ws_v;                 // [S][H][rows][128]
     void* ws_rot;               // [S][rows][64]
     uint32_t* ws_mask;          // [S][rows / 32]: tokens that count
-    uint32_t* ws_odd;           // [S][H][rows / 32]: tokens whose value is not finite
     int32_t rows;               // max_context_len rounded up to whole tiles
     int32_t num_seqs, num_tokens, num_heads, heads_per_cta, block_size, max_blocks_per_seq;
     int64_t num_blocks;
@@ -261,42 +260,43 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         for (int h = 0; h < heads; ++h) {
             const int b = h & 1;
-            uint32_t odd = 0;                             // not 0: some element of V is not finite
+            bool odd = false;                             // some element of V is not finite
             // a wait that gave up is not repeated: the warps walk on together, so
             // that none is left alone at a barrier (PA_STATUS_TIMEOUT)
             if (ok) ok = mbar_poll_warp(o_full + b, (h / 2) & 1);
             tmem_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {                 // 64 columns each: two of K, two of V
+            for (int turn = 0; turn < 4; ++turn) {        // 64 columns each: two of V, two of K
+                const int c = turn ^ 2;
                 uint32_t o[2][32];
                 tmem_ld32(o[0], lanes + b * 256 + c * 64);
                 tmem_ld32(o[1], lanes + b * 256 + c * 64 + 32);
                 tmem_wait_ld();
-                if (c == 3) {
+                if (turn == 3) {
                     tmem_fence_before();
                     mbar_arrive(o_empty + b);
                 }
-                // A token that does not count is a row of zeros: 0 times what its
-                // place holds may not be 0.  So is a value that is not finite: a
-                // query before its token must not meet it, those that see it take
-                // it from ws_odd.
                 uint32_t p[8][4];
-                uint32_t trace = 0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < 32; ++i)
                     p[i >> 2][i & 3] = Elem<T>::from_float2(__uint_as_float(o[i >> 4][2 * i & 31]),
                                                             __uint_as_float(o[i >> 4][(2 * i & 31) + 1]));
-                    trace = add_times_zero<T>(p[i >> 2][i & 3], trace);
-                }
+                // A token that does not count is a row of zeros: 0 times what its
+                // place holds may not be 0.  So is a value that is not finite, for
+                // the queries before its token, whose weight of it is 0; its key
+                // is NaN instead, which those that see the token take over.
                 bool keep = counts;
+                uint32_t other = 0;
                 if (c >= 2) {
-                    odd |= trace;
-                    keep = keep && trace == 0;
-                }
-                if (c == 3) {
-                    const uint32_t word = __ballot_sync(kFullMask, counts && odd != 0);
-                    if (lane == 0)
-                        a.ws_odd[((static_cast<int64_t>(s) * a.num_heads + h0 + h) * a.rows + t) >> 5] = word;
+                    uint32_t z[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) z[i & 3] = add_times_zero<T>(p[i >> 2][i & 3], z[i & 3]);
+                    const bool whole = (z[0] | z[1] | z[2] | z[3]) == 0;
+                    keep = keep && whole;
+                    odd = odd || !whole;
+                } else if (odd) {
+                    keep = false;
+                    other = counts ? 0x7fff7fffu : 0u;    // NaN in both types
                 }
                 // the last box has been read out of shared memory
                 if (r == 0) tma_store_wait_read<0>();
@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     *reinterpret_cast<uint4*>(s_out + r * 128 + ((i ^ (r & 7)) << 4)) =
-                        keep ? make_uint4(p[i][0], p[i][1], p[i][2], p[i][3]) : make_uint4(0, 0, 0, 0);
+                        keep ? make_uint4(p[i][0], p[i][1], p[i][2], p[i][3])
+                             : make_uint4(other, other, other, other);
                 fence_proxy_async_smem();
                 named_barrier(1, 128);
                 if (r == 0) {
@@ -562,13 +563,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const uint32_t s_tmem = tmem + quarter + t * kKvTile;
         const uint32_t o_tmem = tmem + quarter + S::kOCol + t * kValue;
         grid_dependency_wait();                           // the masks are the expansion's
-        const uint32_t* odd_words = a.ws_odd + ((static_cast<int64_t>(s) * a.num_heads + h) * a.rows >> 5);
-        uint32_t any_odd = 0;
-        for (int32_t i = lane; i < n; i += 32) {
-            const uint4 v = reinterpret_cast<const uint4*>(odd_words)[i];
-            any_odd |= v.x | v.y | v.z | v.w;
-        }
-        const bool odd = __any_sync(kFullMask, any_odd != 0);
         float m = -INFINITY, l = 0.f;
         for (int32_t i = 0; i < n; ++i) {
             const int32_t t0 = i * kKvTile;
@@ -638,13 +632,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 tmem_st32(s_tmem + 32 * c, p);
             }
             l += sum.x + sum.y;
-            if (odd) {                                    // a value that is not finite makes NaN
-                for (int k = 0; k < kKvTile / 32; ++k) {
-                    const int32_t ends = last - t0 - 32 * k;      // the last token seen of this word
-                    const uint32_t sees = ends >= 31 ? ~0u : ends < 0 ? 0u : (2u << ends) - 1;
-                    if (odd_words[t0 / 32 + k] & sees) l = NAN;
-                }
-            }
             tmem_wait_st();
             tmem_fence_before();
             mbar_arrive(p_full + t);
@@ -653,7 +640,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         if (ok && n > 0) ok = mbar_poll_warp(pv_done + t, (n - 1) & 1);
         if (ok && n > 0) {
             tmem_fence_after();
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
             // Through shared memory (the tile's queries have been used), 8 KB a
             // warp: stored a row a thread, the 32 lines that each store touches
             // took 9000 cycles.  16-byte chunk j of row r lies at j ^ (r % 8).
