@@ -69,7 +69,7 @@ static pa_status launch_prefill(LatentPrefillArgs& a, const void* query, const v
     const uint64_t w_rows = heads * (kNope + kValue);
     const uint64_t q_bytes = (kNope + kRot) * 2;
     const uint64_t planes = static_cast<uint64_t>(a.num_seqs) * heads;
-    CUtensorMap tm_cache, tm_w, tm_q, tm_k, tm_v, tm_r;
+    CUtensorMap tm_cache, tm_w, tm_q, tm_k, tm_v, tm_r, tm_k_out, tm_v_out;
     if (!encode_rows_map(&tm_cache, a.cache, L + kRot, a.block_size, a.num_blocks, row_bytes,
                          row_bytes * a.block_size, a.block_size) ||
         !encode_rows_map(&tm_w, w_kv, L, w_rows, 1, L * 2, L * 2 * w_rows, 128) ||
@@ -77,6 +77,8 @@ static pa_status launch_prefill(LatentPrefillArgs& a, const void* query, const v
                          kQueryTile) ||
         !encode_rows_map(&tm_k, a.ws_k, kNope, kv_rows, planes, kNope * 2, kNope * 2 * kv_rows, kKvTile) ||
         !encode_rows_map(&tm_v, a.ws_v, kValue, kv_rows, planes, kValue * 2, kValue * 2 * kv_rows, kKvTile) ||
+        !encode_rows_map(&tm_k_out, a.ws_k, kNope, kv_rows, planes, kNope * 2, kNope * 2 * kv_rows, 32, 32) ||
+        !encode_rows_map(&tm_v_out, a.ws_v, kValue, kv_rows, planes, kValue * 2, kValue * 2 * kv_rows, 32, 32) ||
         !encode_rows_map(&tm_r, a.ws_rot, kRot, kv_rows, a.num_seqs, kRot * 2, kRot * 2 * kv_rows, kKvTile))
         return PA_ERR_CUDA;
     const int64_t tiles = a.rows / kKvTile;
@@ -84,8 +86,8 @@ static pa_status launch_prefill(LatentPrefillArgs& a, const void* query, const v
     pa_status st = launch_overlapped(
         expand,
         dim3((a.num_heads + a.heads_per_cta - 1) / a.heads_per_cta, static_cast<unsigned>(tiles), a.num_seqs),
-        dim3(kExpandThreads), E::kSmem, stream, tm_cache, tm_w, tm_k, tm_v,
-        a);
+        dim3(kExpandThreads), E::kSmem, stream, tm_cache, tm_w, tm_k_out,
+        tm_v_out, a);
     if (st != PA_OK) return st;
     const int32_t pairs = (a.max_query_len + 2 * kQueryTile - 1) / (2 * kQueryTile);
     return launch_overlapped(attend, dim3(a.num_heads, pairs, a.num_seqs), dim3(kAttendThreads), S::kSmem,

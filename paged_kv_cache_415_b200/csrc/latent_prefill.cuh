@@ -83,8 +83,8 @@ struct ExpandShape {
     static constexpr int kRowsBytes = kChunks * kKvTile * 128;
     static constexpr int kStageBytes = 128 * 128;   // 64 columns of a head's key or value weights
     static constexpr int kStages = L == 512 ? 5 : 8;
-    static constexpr int kOutBytes = kKvTile * 128; // 64 columns of a result, on their way out
-    static constexpr int kSmem = 1024 + kRowsBytes + kStages * kStageBytes + kOutBytes + 512;
+    static constexpr int kOutBytes = 32 * 64;       // 32 tokens x 32 columns on their way out
+    static constexpr int kSmem = 1024 + kRowsBytes + kStages * kStageBytes + 8 * kOutBytes + 512;
 };
 
 constexpr int kExpandThreads = 192;
@@ -106,7 +106,11 @@ __device__ __forceinline__ uint32_t add_times_zero(uint32_t p, uint32_t z)
 // copies, 5 products; two accumulators of 256 columns (key, value) alternate.
 // Results leave through shared memory by TMA: stored from the registers, a
 // row a thread, the 32 lines that each store touches took as long as the
-// products.
+// products.  Each warp has two boxes of its own for it, so it waits for no other
+// and for the last box but one (4096 tokens, 32 heads, 512 elements: 66.6 k
+// cycles, with one box for all warps 70.8 k).  Without the stores, the products
+// or the weights' copies it is 58 to 62 k each, 34 k being the products' own:
+// the start, with rows from memory, is about 15 k.
 template <typename T, int L>
 __global__ void __launch_bounds__(kExpandThreads, 1)
     latent_expand_kernel(const __grid_constant__ CUtensorMap tm_cache,
@@ -124,7 +128,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     uint8_t* s_rows = smem;
     uint8_t* s_weights = smem + S::kRowsBytes;
     uint8_t* s_out = s_weights + ST * S::kStageBytes;
-    uint64_t* r_full = reinterpret_cast<uint64_t*>(s_out + S::kOutBytes);   // [CH]
+    uint64_t* r_full = reinterpret_cast<uint64_t*>(s_out + 8 * S::kOutBytes);   // [CH]
     uint64_t* w_full = r_full + CH;        // [ST]
     uint64_t* w_empty = w_full + ST;       // [ST]
     uint64_t* o_full = w_empty + ST;       // [2]
@@ -261,61 +265,59 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         for (int h = 0; h < heads; ++h) {
             const int b = h & 1;
             bool odd = false;                             // some element of V is not finite
-            // a wait that gave up is not repeated: the warps walk on together, so
-            // that none is left alone at a barrier (PA_STATUS_TIMEOUT)
+            // a wait that gave up is not repeated (PA_STATUS_TIMEOUT)
             if (ok) ok = mbar_poll_warp(o_full + b, (h / 2) & 1);
             tmem_fence_after();
 #pragma unroll 1
-            for (int turn = 0; turn < 4; ++turn) {        // 64 columns each: two of V, two of K
-                const int c = turn ^ 2;
-                uint32_t o[2][32];
-                tmem_ld32(o[0], lanes + b * 256 + c * 64);
-                tmem_ld32(o[1], lanes + b * 256 + c * 64 + 32);
+            for (int turn = 0; turn < 8; ++turn) {        // 32 columns each: four of V, four of K
+                const int c = turn ^ 4;
+                uint32_t o[32];
+                tmem_ld32(o, lanes + b * 256 + c * 32);
                 tmem_wait_ld();
-                if (turn == 3) {
+                if (turn == 7) {
                     tmem_fence_before();
                     mbar_arrive(o_empty + b);
                 }
-                uint32_t p[8][4];
+                uint32_t p[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    p[i >> 2][i & 3] = Elem<T>::from_float2(__uint_as_float(o[i >> 4][2 * i & 31]),
-                                                            __uint_as_float(o[i >> 4][(2 * i & 31) + 1]));
+                for (int i = 0; i < 16; ++i)
+                    p[i] = Elem<T>::from_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
                 // A token that does not count is a row of zeros: 0 times what its
                 // place holds may not be 0.  So is a value that is not finite, for
                 // the queries before its token, whose weight of it is 0; its key
                 // is NaN instead, which those that see the token take over.
                 bool keep = counts;
                 uint32_t other = 0;
-                if (c >= 2) {
-                    uint32_t z[4] = {0, 0, 0, 0};
+                if (c >= 4) {
+                    uint32_t z[2] = {0, 0};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i & 3] = add_times_zero<T>(p[i >> 2][i & 3], z[i & 3]);
-                    const bool whole = (z[0] | z[1] | z[2] | z[3]) == 0;
+                    for (int i = 0; i < 16; ++i) z[i & 1] = add_times_zero<T>(p[i], z[i & 1]);
+                    const bool whole = (z[0] | z[1]) == 0;
                     keep = keep && whole;
                     odd = odd || !whole;
                 } else if (odd) {
                     keep = false;
                     other = counts ? 0x7fff7fffu : 0u;    // NaN in both types
                 }
-                // the last box has been read out of shared memory
-                if (r == 0) tma_store_wait_read<0>();
-                named_barrier(1, 128);
+                // the last box but one has been read out of shared memory
+                uint8_t* box = s_out + (2 * warp + (turn & 1)) * S::kOutBytes;
+                if (lane == 0) tma_store_wait_read<1>();
+                __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<uint4*>(s_out + r * 128 + ((i ^ (r & 7)) << 4)) =
-                        keep ? make_uint4(p[i][0], p[i][1], p[i][2], p[i][3])
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) =
+                        keep ? make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3])
                              : make_uint4(other, other, other, other);
                 fence_proxy_async_smem();
-                named_barrier(1, 128);
-                if (r == 0) {
-                    tma_store_3d(c < 2 ? &tm_key : &tm_value, (c & 1) * 64, t0,
-                                 s * a.num_heads + h0 + h, s_out);
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_3d(c < 4 ? &tm_key : &tm_value, (c & 3) * 32, t0 + warp * 32,
+                                 s * a.num_heads + h0 + h, box);
                     tma_store_commit();
                 }
             }
         }
-        if (r == 0) tma_store_wait_all();
+        if (lane == 0) tma_store_wait_all();
         if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
     }
     __syncwarp();

@@ -61,21 +61,22 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 }
 
 // A row-major 16-bit matrix [rows][columns] (or, with depth > 1, `depth` of
-// them) whose boxes are 64 columns x box_rows rows, stored with the 128-byte
-// swizzle; columns a multiple of 8, strides of 16 bytes.  What lies outside
-// reads as zero.
+// them) whose boxes are box_columns x box_rows, stored with the swizzle of their
+// width (64 columns: 128 bytes, 32: 64 bytes); columns a multiple of 8, strides
+// of 16 bytes.  What lies outside reads as zero.
 inline bool encode_rows_map(CUtensorMap* map, const void* base, uint64_t columns, uint64_t rows,
                             uint64_t depth, uint64_t row_bytes, uint64_t depth_bytes,
-                            uint32_t box_rows)
+                            uint32_t box_rows, uint32_t box_columns = 64)
 {
     auto enc = tensor_map_encoder();
     if (enc == nullptr) return false;
     const cuuint64_t dims[3] = {columns, rows, depth};
     const cuuint64_t strides[2] = {row_bytes, depth_bytes};
-    const cuuint32_t box[3] = {64u, box_rows, 1u};
+    const cuuint32_t box[3] = {box_columns, box_rows, 1u};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_columns == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
