@@ -10,6 +10,9 @@
 //                         to query_out
 // Each reads its inputs once and writes its outputs once: both are bound by
 // memory for prompts and by launch and load latency for decode steps.
+// Measured: 8192 tokens, 32 + 32 heads of 128 in 80.8 us (5.0 TB/s), 8191
+// latent rows of 576 with 32 heads in 21.1 us (4.2 TB/s), 64 tokens of 32 + 8
+// heads in 2.05 us (from a graph).
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math.h>
@@ -175,7 +178,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
 }
 
 // Rows a lane group takes: as many (1, 2 or 4) as leave enough warps to fill
-// the GPU, kFillWarps.
+// the GPU, kFillWarps.  (8192 tokens, 32 + 32 heads: 131 us with 1, 87 with 2,
+// 76 with 4, more with 6 or 8; where the warps are few, more rows a group only
+// lengthen its chain.)
 constexpr int64_t kFillWarps = 148 * 32;
 
 template <typename T, typename Store, int D, int ROWS>
