@@ -89,9 +89,13 @@ static pa_status launch_prefill(LatentPrefillArgs& a, const void* query, const v
         dim3(kExpandThreads), E::kSmem, stream, tm_cache, tm_w, tm_k_out,
         tm_v_out, a);
     if (st != PA_OK) return st;
-    const int32_t pairs = (a.max_query_len + 2 * kQueryTile - 1) / (2 * kQueryTile);
-    return launch_overlapped(attend, dim3(a.num_heads, pairs, a.num_seqs), dim3(kAttendThreads), S::kSmem,
-                             stream, tm_q, tm_k, tm_v, tm_r, a);
+    a.pairs = (a.max_query_len + 2 * kQueryTile - 1) / (2 * kQueryTile);
+    const int64_t items = static_cast<int64_t>(a.pairs) * a.num_seqs;
+    // (where all blocks run at once their order does not matter)
+    a.sorted = a.num_seqs > 1 && items <= kSortItems && items * a.num_heads > sm_count();
+    const dim3 grid = a.sorted ? dim3(a.num_heads, static_cast<unsigned>(items))
+                               : dim3(a.num_heads, a.pairs, a.num_seqs);
+    return launch_overlapped(attend, grid, dim3(kAttendThreads), S::kSmem, stream, tm_q, tm_k, tm_v, tm_r, a);
 }
 
 }  // namespace pa
