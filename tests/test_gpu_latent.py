@@ -486,3 +486,24 @@ def test_prefill_value_past_the_type():
     safe[0] = 0
     ref, bound = latent_prefill(query, cache, safe, tables, starts, ctx, 0.07)
     assert_within(out[:, 1], ref[:, 1], bound[:, 1], "other head")
+
+
+@pytest.mark.parametrize("heads,new,old", [
+    (20, [1, 300, 300, 0, 513, 129, 17], [0, 40, 40, 0, 3, 400, 290]),    # ranked by size, with ties
+    (40, [3, 2, 1, 4], [70, 0, 200, 5]),                                  # a pair a sequence
+    (2, [1 + i % 5 for i in range(150)], [i % 3 for i in range(150)]),    # too many to rank
+])
+def test_prefill_many_blocks(heads, new, old):
+    """More blocks than fit at once: the order in which they are taken is of
+    no account, a bad length among them neither."""
+    x = _prompt(heads, 256, 16, new, old, torch.bfloat16, 31)
+    ctx = x[-1].clone()
+    ctx[1] = -7
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    top = int(x[-1].max())
+    out = _prefill(*x[:-1], ctx, 192 ** -0.5, max_context=top, status=status).cpu()
+    first = new[0]
+    assert (out[first:first + new[1]] == 0).all() and int(status) == BAD_CONTEXT
+    ctx[1] = 0
+    ref, bound = latent_prefill(*x[:-1], ctx, 192 ** -0.5)
+    assert_within(out, ref, bound, "prefill")
