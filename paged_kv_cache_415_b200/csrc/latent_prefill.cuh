@@ -13,9 +13,9 @@
 //
 // The expansion costs 2 L 256 operations a token and head, the attention 2 (192
 // + 128) a query, visible token and head.  Measured at 4096 new tokens, 32
-// heads, L 512: 39.2 us (0.88 PFLOP/s) and 177 us (0.97 PFLOP/s), of 1.64 that
-// products alone reach here; the attention is held by the chain of its softmax,
-// then by the power limit.
+// heads, L 512: 39.2 us (0.88 PFLOP/s) and 162 us (1.06 PFLOP/s), of 1.64 that
+// products alone reach here.  The attention's products take 3480 of its 3700
+// cycles a step, as scores of 64 keys at a time read shared memory at its rate.
 //
 // Roundings: K, V and the weights P go to the pool's 16-bit type, as the
 // products' operands must be of one such type; sums and softmax are fp32.  V's
@@ -352,10 +352,11 @@ struct AttendShape {
 };
 
 constexpr int kAttendThreads = 352;
+constexpr int kHalf = kKvTile / 2;              // keys whose scores and weights are under way at once
 constexpr int kSortItems = 128;                 // pairs of query tiles at most that are sorted
 
 // How long pair `item` of the query tiles takes, about: a step of both tiles
-// costs 4100 cycles, of one alone 2900.
+// costs about 41, of one alone 29.
 __device__ __forceinline__ int32_t attend_size(const LatentPrefillArgs& a, int32_t item)
 {
     const PromptSpan p = prompt_span(a, item / a.pairs);
@@ -370,17 +371,22 @@ __device__ __forceinline__ int32_t attend_size(const LatentPrefillArgs& a, int32
 
 // Grid (head, pair of query tiles of a sequence), the longest pairs first: by
 // size over all sequences where they are few enough to rank (7 prompts of 1 to
-// 700 tokens behind up to 2300, 20 heads: 95 us, in the sequences' order 107),
+// 700 tokens behind up to 2300, 20 heads: 97 us, in the sequences' order 107),
 // else within a sequence.  Warps:
 // 0-3 and 4-7 softmax of one query tile each, a thread a query; 8 copies; 9
-// and 10 the products of one query tile each.  While one tile's scores go
-// through the softmax, the products of the other run; with a warp each, one
-// tile's waits do not hold up the other's products (with one warp for both the
-// tensor cores stood still 480 cycles a step).
+// and 10 the products of one query tile each (with one warp for both the tensor
+// cores stood still 480 cycles a step).
+//
+// A tile of keys goes through in two halves of 64: while the softmax has one,
+// the scores of the other are made, so that it never waits for them.  Weights
+// take the first half of their scores' place, and the scores of the next half
+// but one follow them there.  (4096 tokens, 32 heads: 264 k cycles; 128 keys at
+// once, whose scores have no second place in TMEM, 290 k, though products of 64
+// columns take 50 cycles and of 128 only 66.)
 //
 // Tile i of the keys takes slots 5 i .. 5 i + 2 of the ring (modulo 8), its
 // values the two after them.  So K_i follows K_{i-2} and V_{i-2}, and V_i
-// follows K_{i-1}, which is free as soon as its scores are taken: the values
+// follows K_{i-1}, which is free as soon as its scores are made: the values
 // lie there when their weights are ready.  (With two buffers for K and one for
 // V every step waited 700 cycles for its values.)
 template <typename T>
@@ -402,10 +408,10 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     uint64_t* k_empty = k_full + 2;        // [2]
     uint64_t* v_full = k_empty + 2;        // [2]
     uint64_t* v_empty = v_full + 2;        // [2]
-    uint64_t* s_full = v_empty + 2;        // [2]
-    uint64_t* p_full = s_full + 2;         // [2]
-    uint64_t* pv_done = p_full + 2;        // [2]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pv_done + 2);
+    uint64_t* s_full = v_empty + 2;        // [2][2], of a query tile's halves
+    uint64_t* p_full = s_full + 4;         // [2][2]
+    uint64_t* pv_done = p_full + 4;        // [2][2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pv_done + 4);
     int32_t* begun = reinterpret_cast<int32_t*>(tmem_slot + 1);   // the first tile's first weights
 
     const int warp = __shfl_sync(kFullMask, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -473,11 +479,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             mbar_init(q_full + i, 1);
             mbar_init(k_full + i, 1);
             mbar_init(k_empty + i, 2);                    // both tiles' products
+            mbar_init(v_full + i, 1);
+            mbar_init(v_empty + i, 2);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 128);
             mbar_init(pv_done + i, 1);
-            mbar_init(v_full + i, 1);
-            mbar_init(v_empty + i, 2);
         }
         *begun = 0;
         fence_barrier_init();
@@ -541,64 +549,83 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     } else if (warp >= 9) {
         const int t = warp - 9;
         const int32_t n = steps[t];
-        const uint32_t idesc_s = mma_desc<T>(kQueryTile, kKvTile);
+        const uint32_t idesc_s = mma_desc<T>(kQueryTile, kHalf);
         const uint32_t idesc_o = mma_desc<T>(kQueryTile, 64, false, true);
         const uint32_t query = smem_u32(s_query) + t * S::kQueryBytes, ring = smem_u32(s_ring);
-        // Scores of tile i of the keys, which has arrived; past the tile's last
-        // step the room is let go of all the same (not before the keys are
-        // there: a release a step, or the copies would run ahead).
-        auto scores = [&](int32_t i) {
-            if (i >= n) {
-                if (leader) mbar_arrive(k_empty + (i & 1));
-                return;
-            }
+        // Scores of half j of the keys (of tile j / 2, which has arrived).
+        auto scores = [&](int32_t j) {
+            const int half = j & 1;
 #pragma unroll
             for (int c = 0; c < S::kChunks; ++c) {
                 const uint64_t da = desc_k_major(query + c * kQueryTile * 128);
-                const uint64_t db = desc_k_major(ring + (5 * i + c) % S::kSlots * S::kSlotBytes);
+                const uint64_t db = desc_k_major(ring + (5 * (j >> 1) + c) % S::kSlots * S::kSlotBytes +
+                                                 half * kHalf * 128);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_ss(tmem + t * kKvTile, da + 2 * k, db + 2 * k, idesc_s, c + k > 0, leader);
+                    mma_ss(tmem + t * kKvTile + half * kHalf, da + 2 * k, db + 2 * k, idesc_s, c + k > 0,
+                           leader);
             }
             if (leader) {
-                mma_commit(s_full + t);
-                mma_commit(k_empty + (i & 1));
+                mma_commit(s_full + 2 * t + half);
+                if (half) mma_commit(k_empty + ((j >> 1) & 1));
+            }
+        };
+        // The weights of half j times its values.
+        auto values = [&](int32_t j) {
+            const int half = j & 1;
+#pragma unroll
+            for (int c = 0; c < S::kValueSlots; ++c) {
+                const uint64_t db = desc_mn_major(
+                    ring + (5 * (j >> 1) + 3 + c) % S::kSlots * S::kSlotBytes + half * kHalf * 128,
+                    S::kSlotBytes);
+#pragma unroll
+                for (int k = 0; k < kHalf / 16; ++k)
+                    mma_ts(tmem + S::kOCol + t * kValue + c * 64, tmem + t * kKvTile + half * kHalf + k * 8,
+                           db + k * (2048 >> 4), idesc_o, j + k > 0, leader);
+            }
+            if (leader) {
+                mma_commit(pv_done + 2 * t + half);
+                if (half) mma_commit(v_empty + ((j >> 1) & 1));
             }
         };
         ok = (n == 0 || mbar_poll_warp(q_full + t, 0)) && mbar_poll_warp(k_full, 0);
-        // The second tile starts when the first one's weights are out: half a
-        // step apart their softmax and products alternate; side by side they
-        // stayed so for ten steps, 5400 cycles each instead of 3700.
+        // The second tile starts when the first one's weights are out: apart,
+        // their softmax and products alternate.
         if (t == 1 && n > 0)
             for (int i = 0; i < 4096 && !__all_sync(kFullMask, *static_cast<volatile int32_t*>(begun) != 0); ++i)
                 __nanosleep(20);
-        if (ok) scores(0);
-        for (int32_t i = 0; i < total && ok; ++i) {
-            // values and next keys are looked for before the weights: they are there first
-            ok = mbar_poll_warp(v_full + (i & 1), (i / 2) & 1) &&
-                 (i + 1 >= total || mbar_poll_warp(k_full + ((i + 1) & 1), ((i + 1) / 2) & 1)) &&
-                 (i >= n || mbar_poll_warp(p_full + t, i & 1));
+        if (ok && n > 0) {
+            scores(0);
+            scores(1);
+        } else if (ok && leader) {
+            mbar_arrive(k_empty);
+        }
+        // Past the tile's last step the room is let go of all the same (not
+        // before the copies are there: a release a step, or they would run ahead).
+        for (int32_t i = 0; i < total; ++i) {
+            ok = ok && mbar_poll_warp(v_full + (i & 1), (i / 2) & 1) &&
+                 (i >= n || mbar_poll_warp(p_full + 2 * t, i & 1));
             if (!ok) break;
             tmem_fence_after();
+            // S of the next half in the same place takes that of P: products run in order
+            if (i < n) values(2 * i);
+            if (i + 1 < total) {
+                ok = mbar_poll_warp(k_full + ((i + 1) & 1), ((i + 1) / 2) & 1);
+                if (!ok) break;
+                if (i + 1 < n)
+                    scores(2 * i + 2);
+                else if (leader)
+                    mbar_arrive(k_empty + ((i + 1) & 1));
+            }
             if (i < n) {
-#pragma unroll
-                for (int c = 0; c < S::kValueSlots; ++c) {
-                    const uint64_t db = desc_mn_major(
-                        ring + (5 * i + 3 + c) % S::kSlots * S::kSlotBytes, S::kSlotBytes);
-#pragma unroll
-                    for (int k = 0; k < kKvTile / 16; ++k)
-                        mma_ts(tmem + S::kOCol + t * kValue + c * 64, tmem + t * kKvTile + k * 8,
-                               db + k * (2048 >> 4), idesc_o, i + k > 0, leader);
-                }
-                if (leader) {
-                    mma_commit(pv_done + t);
-                    mma_commit(v_empty + (i & 1));
-                }
+                ok = mbar_poll_warp(p_full + 2 * t + 1, i & 1);
+                if (!ok) break;
+                tmem_fence_after();
+                values(2 * i + 1);
+                if (i + 1 < n) scores(2 * i + 3);
             } else if (leader) {
                 mbar_arrive(v_empty + (i & 1));
             }
-            // S of the next tile takes the place of P: products run in order
-            if (i + 1 < total) scores(i + 1);
         }
         if (!ok && lane == 0) status_or(a.d_status, PA_STATUS_TIMEOUT);
     } else {
@@ -612,25 +639,26 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const uint32_t o_tmem = tmem + quarter + S::kOCol + t * kValue;
         grid_dependency_wait();                           // the masks are the expansion's
         float m = -INFINITY, l = 0.f;
-        for (int32_t i = 0; i < n; ++i) {
-            const int32_t t0 = i * kKvTile;
-            const uint4 word = *reinterpret_cast<const uint4*>(a.ws_mask +
+        for (int32_t j = 0; j < 2 * n; ++j) {
+            const int half = j & 1;
+            const int32_t t0 = j * kHalf;
+            const uint2 word = *reinterpret_cast<const uint2*>(a.ws_mask +
                                                                ((static_cast<int64_t>(s) * a.rows + t0) >> 5));
-            ok = mbar_poll_warp(s_full + t, i & 1);
+            ok = mbar_poll_warp(s_full + 2 * t + half, (j >> 1) & 1);
             if (!ok) break;
             tmem_fence_after();
-            uint32_t x[kKvTile];
+            uint32_t x[kHalf];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                tmem_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * c), s_tmem + 32 * c);
+            for (int c = 0; c < kHalf / 32; ++c)
+                tmem_ld32(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * c), s_tmem + half * kHalf + 32 * c);
             tmem_wait_ld();
             float unit = a.scale_log2;
-            const bool whole = (word.x & word.y & word.z & word.w) == ~0u && last - t0 >= kKvTile - 1;
+            const bool whole = (word.x & word.y) == ~0u && last - t0 >= kHalf - 1;
             if (!__all_sync(kFullMask, whole) || unit < 0.f) {
                 // scaled here: a masked score is -inf whatever the scale
-                const uint32_t words[4] = {word.x, word.y, word.z, word.w};
+                const uint32_t words[2] = {word.x, word.y};
 #pragma unroll
-                for (int e = 0; e < kKvTile; ++e) {
+                for (int e = 0; e < kHalf; ++e) {
                     const bool sees = e <= last - t0 && (words[e >> 5] >> (e & 31) & 1);
                     x[e] = __float_as_uint(sees ? __uint_as_float(x[e]) * unit : -INFINITY);
                 }
@@ -638,7 +666,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             }
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < kKvTile; e += 2)
+            for (int e = 0; e < kHalf; e += 2)
                 top[e >> 1 & 3] = max3(top[e >> 1 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
             const float peak = max3(top[0], top[1], fmaxf(top[2], top[3])) * unit;
             // The reference moves where it is unset or passed by 2^8.
@@ -647,8 +675,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 const float f = moves ? exp2_fast(m - peak) : 1.f;
                 if (moves) m = peak;
                 l *= f;
-                if (i > 0) {
-                    ok = mbar_poll_warp(pv_done + t, (i - 1) & 1);
+                if (j > 0) {
+                    ok = mbar_poll_warp(pv_done + 2 * t + (half ^ 1), ((j - 1) >> 1) & 1);
                     if (!ok) break;
                     tmem_fence_after();
 #pragma unroll 1
@@ -666,26 +694,23 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const float sub = m == -INFINITY ? 0.f : m;
             float2 sum = make_float2(0.f, 0.f);
             const float2 unit2 = make_float2(unit, unit), sub2 = make_float2(-sub, -sub);
+            uint32_t p[kHalf / 2];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t p[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float2 y = fma2(make_float2(__uint_as_float(x[64 * c + 2 * e]),
-                                                      __uint_as_float(x[64 * c + 2 * e + 1])), unit2, sub2);
-                    const float2 w = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                    sum = add2(sum, w);
-                    p[e] = Elem<T>::from_float2(w.x, w.y);
-                }
-                tmem_st32(s_tmem + 32 * c, p);
+            for (int e = 0; e < kHalf / 2; ++e) {
+                const float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
+                                      unit2, sub2);
+                const float2 w = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                sum = add2(sum, w);
+                p[e] = Elem<T>::from_float2(w.x, w.y);
             }
+            tmem_st32(s_tmem + half * kHalf, p);
             l += sum.x + sum.y;
             tmem_wait_st();
             tmem_fence_before();
-            mbar_arrive(p_full + t);
-            if (i == 0 && threadIdx.x == 0) *static_cast<volatile int32_t*>(begun) = 1;
+            mbar_arrive(p_full + 2 * t + half);
+            if (j == 0 && threadIdx.x == 0) *static_cast<volatile int32_t*>(begun) = 1;
         }
-        if (ok && n > 0) ok = mbar_poll_warp(pv_done + t, (n - 1) & 1);
+        if (ok && n > 0) ok = mbar_poll_warp(pv_done + 2 * t + 1, (n - 1) & 1);
         if (ok && n > 0) {
             tmem_fence_after();
             const float inv = l > 0.f ? 1.f / l : 0.f;
