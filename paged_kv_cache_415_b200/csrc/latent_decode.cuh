@@ -31,7 +31,7 @@
 //
 // Measured: 256 sequences of 3500 to 4500 tokens, 16 heads, in 204.7 us of this
 // kernel (1.20 GB, 5.9 TB/s: memory); 64 sequences to 4096 tokens, 128 heads,
-// in 97.6 us with the sum (0.42 PFLOP/s: the chain of a tile's copies, scores,
+// in 95.7 us with the sum (0.42 PFLOP/s: the chain of a tile's copies, scores,
 // softmax and sums, with room for two tiles).
 #pragma once
 

