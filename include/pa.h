@@ -728,8 +728,10 @@ PA_API pa_status pa_latent_decode(void* out, const void* query, const void* cach
  * tokens at positions up to context_lens[s] - n + i:
  *   x_t = scale * (q_nope . K_nope_t + q_rope . r_t),
  *   out = sum_t softmax(x)_t V_t.
- * A query that sees a token of which some element of V (rounded to 16 bits) is
- * not finite gives NaN in that head; queries before the token do not meet it.
+ * A query that sees a token of which some element of V is not finite gives NaN
+ * in that head; queries before the token do not meet it.  K is rounded to
+ * `dtype`, V to fp16 with a power of two a head and 32 tokens (any finite V has
+ * a place, elements 2^-14 of the largest of the 32 keep fewer bits).
  *
  * out            [num_tokens][num_heads][value_dim], 16-byte aligned; written
  *                for the rows of the sequences, others are left as they were.

@@ -16,11 +16,12 @@
 namespace pa {
 
 // The workspace: K and V of every head, the rotated part, one mask bit a
-// token; a sequence's rows are whole tiles of keys.
+// token and one exponent a head and 32 tokens; a sequence's rows are whole tiles
+// of keys.
 struct PrefillSpace {
     int64_t rows;
-    size_t key_bytes, rot_bytes, mask_bytes;
-    size_t total() const { return 2 * key_bytes + rot_bytes + mask_bytes; }
+    size_t key_bytes, rot_bytes, mask_bytes, exp_bytes;
+    size_t total() const { return 2 * key_bytes + rot_bytes + mask_bytes + exp_bytes; }
 };
 
 static PrefillSpace prefill_space(int32_t num_seqs, int32_t num_heads, int32_t max_context_len)
@@ -31,6 +32,7 @@ static PrefillSpace prefill_space(int32_t num_seqs, int32_t num_heads, int32_t m
     s.key_bytes = all * num_heads * kNope * 2;
     s.rot_bytes = all * kRot * 2;
     s.mask_bytes = all / 8;
+    s.exp_bytes = all / 32 * num_heads * 4;
     return s;
 }
 
@@ -155,6 +157,7 @@ extern "C" pa_status pa_latent_prefill(
     a.ws_v = ws + sp.key_bytes;
     a.ws_rot = ws + 2 * sp.key_bytes;
     a.ws_mask = reinterpret_cast<uint32_t*>(ws + 2 * sp.key_bytes + sp.rot_bytes);
+    a.ws_exp = reinterpret_cast<float*>(ws + 2 * sp.key_bytes + sp.rot_bytes + sp.mask_bytes);
     a.rows = static_cast<int32_t>(sp.rows);
     a.num_seqs = num_seqs;
     a.num_tokens = num_tokens;

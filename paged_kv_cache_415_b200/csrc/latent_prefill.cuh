@@ -17,11 +17,13 @@
 // products alone reach here.  The attention's products take 3480 of its 3700
 // cycles a step, as scores of 64 keys at a time read shared memory at its rate.
 //
-// Roundings: K, V and the weights P go to the pool's 16-bit type, as the
-// products' operands must be of one such type; sums and softmax are fp32.  V's
-// and P's add about as much to the output's error as its own rounding (bf16:
-// 0.0027 of the output in all, its own 0.0017).  A second 16-bit part of either
-// would take that away for two fifths more products.
+// Roundings: sums and softmax are fp32.  K goes to the pool's type, as the
+// queries are of it and the operands of a product are of one type.  V and the
+// weights P go to fp16, with a power of two a head and 32 tokens: bf16 for them
+// added as much error each as the output's own rounding (0.0027 of the output
+// in all, its own 0.0017; with fp16 0.0020, for 1 % of the time), and no finite
+// value passes the type.  A token whose values are 2^14 below the largest of its
+// 32 begins to lose bits.
 #pragma once
 
 #include <cuda.h>
@@ -51,6 +53,7 @@ struct LatentPrefillArgs {
     void* ws_v;                 // [S][H][rows][128]
     void* ws_rot;               // [S][rows][64]
     uint32_t* ws_mask;          // [S][rows / 32]: tokens that count
+    float* ws_exp;              // [S][H][rows / 32]: V of 32 tokens is kept times 2^-this
     int32_t rows;               // max_context_len rounded up to whole tiles
     int32_t num_seqs, num_tokens, num_heads, heads_per_cta, block_size, max_blocks_per_seq;
     int64_t num_blocks;
@@ -98,17 +101,13 @@ struct ExpandShape {
 };
 
 constexpr int kExpandThreads = 192;
+constexpr int kLeastExp = -60;                  // values below 2^-60 are kept as if they were that large
 
-// z + 0 p on pairs: a z that begins at 0 stays 0 unless some element of some p
-// is not finite.
-template <typename T>
-__device__ __forceinline__ uint32_t add_times_zero(uint32_t p, uint32_t z)
+// The larger magnitude, or NaN.
+__device__ __forceinline__ float max_abs_nan(float a, float b)
 {
-    uint32_t d;
-    if constexpr (std::is_same<T, __half>::value)
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(p), "r"(0u), "r"(z));
-    else
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(p), "r"(0u), "r"(z));
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
     return d;
 }
 
@@ -274,10 +273,31 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         for (int h = 0; h < heads; ++h) {
             const int b = h & 1;
-            bool odd = false;                             // some element of V is not finite
             // a wait that gave up is not repeated (PA_STATUS_TIMEOUT)
             if (ok) ok = mbar_poll_warp(o_full + b, (h / 2) & 1);
             tmem_fence_after();
+            // V is kept in fp16 whatever the pool's type, the 32 tokens of a warp
+            // times a power of two that brings their largest element below 1.
+            float high = 0.f;
+#pragma unroll 1
+            for (int c = 4; c < 8; ++c) {
+                uint32_t o[32];
+                tmem_ld32(o, lanes + b * 256 + c * 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) high = max_abs_nan(high, __uint_as_float(o[i]));
+            }
+            // A token that does not count is a row of zeros: 0 times what its place
+            // holds may not be 0.  So is a value that is not finite, for the queries
+            // before its token, whose weight of it is 0; its key is NaN instead,
+            // which those that see the token take over.
+            const bool odd = !(high < INFINITY);
+            const uint32_t most = __reduce_max_sync(kFullMask, counts && !odd ? __float_as_uint(high) : 0u);
+            const int ex = min(max(static_cast<int>(most >> 23) - 126, kLeastExp), 126);
+            const float unit = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+            if (lane == 0)
+                a.ws_exp[((static_cast<int64_t>(s) * a.num_heads + h0 + h) * a.rows + t) >> 5] =
+                    static_cast<float>(ex);
 #pragma unroll 1
             for (int turn = 0; turn < 8; ++turn) {        // 32 columns each: four of V, four of K
                 const int c = turn ^ 4;
@@ -290,25 +310,13 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                 }
                 uint32_t p[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    p[i] = Elem<T>::from_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-                // A token that does not count is a row of zeros: 0 times what its
-                // place holds may not be 0.  So is a value that is not finite, for
-                // the queries before its token, whose weight of it is 0; its key
-                // is NaN instead, which those that see the token take over.
-                bool keep = counts;
-                uint32_t other = 0;
-                if (c >= 4) {
-                    uint32_t z[2] = {0, 0};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) z[i & 1] = add_times_zero<T>(p[i], z[i & 1]);
-                    const bool whole = (z[0] | z[1]) == 0;
-                    keep = keep && whole;
-                    odd = odd || !whole;
-                } else if (odd) {
-                    keep = false;
-                    other = counts ? 0x7fff7fffu : 0u;    // NaN in both types
+                for (int i = 0; i < 16; ++i) {
+                    const float lo = __uint_as_float(o[2 * i]), hi = __uint_as_float(o[2 * i + 1]);
+                    p[i] = c >= 4 ? Elem<__half>::from_float2(lo * unit, hi * unit)
+                                  : Elem<T>::from_float2(lo, hi);
                 }
+                const bool keep = counts && !odd;
+                const uint32_t other = counts && c < 4 ? 0x7fff7fffu : 0u;      // NaN in both types
                 // the last box but one has been read out of shared memory
                 uint8_t* box = s_out + (2 * warp + (turn & 1)) * S::kOutBytes;
                 if (lane == 0) tma_store_wait_read<1>();
@@ -550,7 +558,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const int t = warp - 9;
         const int32_t n = steps[t];
         const uint32_t idesc_s = mma_desc<T>(kQueryTile, kHalf);
-        const uint32_t idesc_o = mma_desc<T>(kQueryTile, 64, false, true);
+        const uint32_t idesc_o = mma_desc<__half>(kQueryTile, 64, false, true);
         const uint32_t query = smem_u32(s_query) + t * S::kQueryBytes, ring = smem_u32(s_ring);
         // Scores of half j of the keys (of tile j / 2, which has arrived).
         auto scores = [&](int32_t j) {
@@ -644,6 +652,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const int32_t t0 = j * kHalf;
             const uint2 word = *reinterpret_cast<const uint2*>(a.ws_mask +
                                                                ((static_cast<int64_t>(s) * a.rows + t0) >> 5));
+            const float2 ex = *reinterpret_cast<const float2*>(
+                a.ws_exp + (((static_cast<int64_t>(s) * a.num_heads + h) * a.rows + t0) >> 5));
             ok = mbar_poll_warp(s_full + 2 * t + half, (j >> 1) & 1);
             if (!ok) break;
             tmem_fence_after();
@@ -667,8 +677,13 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int e = 0; e < kHalf; e += 2)
-                top[e >> 1 & 3] = max3(top[e >> 1 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-            const float peak = max3(top[0], top[1], fmaxf(top[2], top[3])) * unit;
+                top[(e >> 1 & 1) + 2 * (e >> 5)] =
+                    max3(top[(e >> 1 & 1) + 2 * (e >> 5)], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+            // Weights take the powers of two of their values along: w = 2^(x + ex - m),
+            // so m follows the largest product of a weight and a value, and
+            //   out = sum w V' / sum w 2^-ex.
+            const float peak = fmaxf(fmaf(fmaxf(top[0], top[1]), unit, ex.x),
+                                     fmaf(fmaxf(top[2], top[3]), unit, ex.y));
             // The reference moves where it is unset or passed by 2^8.
             const bool moves = peak > m + 8.0f;
             if (__any_sync(kFullMask, moves)) {
@@ -692,19 +707,20 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 }
             }
             const float sub = m == -INFINITY ? 0.f : m;
-            float2 sum = make_float2(0.f, 0.f);
-            const float2 unit2 = make_float2(unit, unit), sub2 = make_float2(-sub, -sub);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 unit2 = make_float2(unit, unit);
+            const float2 add[2] = {make_float2(ex.x - sub, ex.x - sub), make_float2(ex.y - sub, ex.y - sub)};
             uint32_t p[kHalf / 2];
 #pragma unroll
             for (int e = 0; e < kHalf / 2; ++e) {
                 const float2 y = fma2(make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])),
-                                      unit2, sub2);
+                                      unit2, add[e >> 4]);
                 const float2 w = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                sum = add2(sum, w);
-                p[e] = Elem<T>::from_float2(w.x, w.y);
+                sum[e >> 4] = add2(sum[e >> 4], w);
+                p[e] = Elem<__half>::from_float2(w.x, w.y);
             }
             tmem_st32(s_tmem + half * kHalf, p);
-            l += sum.x + sum.y;
+            l += (sum[0].x + sum[0].y) * exp2_fast(-ex.x) + (sum[1].x + sum[1].y) * exp2_fast(-ex.y);
             tmem_wait_st();
             tmem_fence_before();
             mbar_arrive(p_full + 2 * t + half);

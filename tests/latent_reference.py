@@ -78,13 +78,17 @@ def context_rows(cache, table, ctx):
     return rows, ok
 
 
-def attend(q, keys, values, seen, scale, dtype, key_slack=None, value_slack=0.0):
+def attend(q, keys, values, seen, scale, dtype, key_slack=None, value_slack=0.0, scaled=False):
     """(out, bound) of softmax(scale q keys^T) values for q [n][D], keys
     [t][D], values [t][E], seen [n][t].  The bound: score errors of at most
     e = scale * (D 2^-23 |q| |k| + |q| key_slack) change a weight by a factor
     within exp(2 e); weights and values rounded to the type, the fp16 weights
-    also to multiples of 2^-24 of the largest; sums of t terms."""
+    also to multiples of 2^-24 of the largest; sums of t terms.  `scaled`: weights
+    and values in fp16 with the values' powers of two, so a weight times its
+    values' power (at most twice their largest magnitude) is rounded by 2^-11, or
+    by 2^-25 of the largest such product."""
     u = half_step(dtype)
+    u_w = 2.0 ** -11 if scaled else u
     score = (q @ keys.T) * scale
     e = (q.abs() @ keys.abs().T) * (q.shape[1] * 2.0 ** -23)
     if key_slack is not None:
@@ -99,10 +103,12 @@ def attend(q, keys, values, seen, scale, dtype, key_slack=None, value_slack=0.0)
     out = p @ values
     mass = p @ values.abs()
     t = keys.shape[0]
-    rel = u + torch.expm1(2 * e) + (t + 8) * 2.0 ** -23
+    rel = u_w + torch.expm1(2 * e) + (t + 8) * 2.0 ** -23
     bound = rel * mass + p @ torch.broadcast_to(torch.as_tensor(value_slack, dtype=F64),
                                                 values.shape)
-    if dtype == torch.float16:
+    if scaled:
+        bound = bound + t * 2.0 ** -24 * values.abs().amax()
+    elif dtype == torch.float16:
         bound = bound + t * 2.0 ** -25 * values.abs().amax(0, keepdim=True)
     return out, bound * (1 + u) + u * out.abs() + tiny_step(dtype)
 
@@ -147,11 +153,14 @@ def latent_prefill(query, cache, w_kv, tables, starts, context_lens, scale):
         for h in range(heads):
             w = w_kv[h].to(F64)
             kv = rows[:, :lat] @ w.T
-            # the expanded key or value: a sum of `lat` products rounded to the type
-            slack = u * kv.abs() + (lat * 2.0 ** -23) * (rows[:, :lat].abs() @ w.abs().T) \
-                + tiny_step(dtype)
+            # the expanded key: a sum of `lat` products rounded to the type; the value:
+            # to fp16 below the power of two over its largest of 32 tokens, or all
+            sums = (lat * 2.0 ** -23) * (rows[:, :lat].abs() @ w.abs().T)
+            slack = u * kv.abs() + sums + tiny_step(dtype)
+            slack[:, 128:] = 2.0 ** -11 * kv[:, 128:].abs() + sums[:, 128:] \
+                + 2.0 ** -24 * kv[:, 128:].abs().amax()
             key = torch.cat([kv[:, :128], rows[:, lat:]], 1)
             key_slack = torch.cat([slack[:, :128], torch.zeros_like(rows[:, lat:])], 1)
             out[a:b, h], bound[a:b, h] = attend(query[a:b, h].to(F64), key, kv[:, 128:], seen,
-                                                scale, dtype, key_slack, slack[:, 128:])
+                                                scale, dtype, key_slack, slack[:, 128:], True)
     return out, bound

@@ -475,17 +475,49 @@ def test_prefill_later_tokens_do_not_reach_back(dtype, worst):
 
 
 def test_prefill_value_past_the_type():
-    """A value of one head past the type's range: that head's queries alone."""
+    """A value past fp16, that its context's mean is not: as any other."""
     x = _prompt(2, 512, 32, [60], [40], torch.float16, 22)
     query, cache, w, tables, starts, ctx = x
     # head 0's value element 5 of token 20 is about 300 * 512 * 0.8, of others 300 * 512^0.5
     w[0, 128 + 5] = torch.where(cache[tables[0, 0], 20, :512] < 0, -300.0, 300.0).half()
     out = _prefill(*x, 0.07).cpu()
-    assert torch.isnan(out[:, 0]).all()
-    safe = w.clone()
-    safe[0] = 0
-    ref, bound = latent_prefill(query, cache, safe, tables, starts, ctx, 0.07)
-    assert_within(out[:, 1], ref[:, 1], bound[:, 1], "other head")
+    ref, bound = latent_prefill(*x, 0.07)
+    assert ref.abs().max() < 60000
+    assert_within(out, ref, bound, "prefill")
+
+
+@pytest.mark.parametrize("power", [-40, 40])
+def test_prefill_follows_the_values_scale(power):
+    """Values times a power of two give outputs times it, and are of no account
+    for the other heads."""
+    x = _prompt(3, 256, 16, [150, 33], [20, 70], torch.bfloat16, 23)
+    query, cache, w, tables, starts, ctx = x
+    out = _prefill(*x, 0.07)
+    ref, bound = latent_prefill(*x, 0.07)
+    w[1, 128:] = torch.ldexp(w[1, 128:].float(), torch.tensor(power)).bfloat16()
+    got = _prefill(query, cache, w, tables, starts, ctx, 0.07)
+    assert torch.equal(got[:, ::2], out[:, ::2])
+    assert_within(torch.ldexp(got[:, 1].cpu().to(F64), torch.tensor(-power)), ref[:, 1],
+                  bound[:, 1], "scaled")
+
+
+def test_prefill_values_of_uneven_size():
+    """Tokens whose values differ by powers of two up to 2^12, within the 32
+    that share one and between them; a context whose values are all zero."""
+    x = _prompt(2, 256, 16, [200, 20], [30, 0], torch.bfloat16, 24)
+    query, cache, w, tables, starts, ctx = x
+    t = torch.arange(230)
+    grow = torch.where(t < 100, t % 7, t % 13).float()
+    rows = cache[tables[0][t // 16].long(), t % 16]
+    rows[:, :256] = (rows[:, :256].float() * 2.0 ** grow[:, None] / 64).bfloat16()
+    cache[tables[0][t // 16].long(), t % 16] = rows
+    w[:, :128] /= 64                                   # (scores of an ordinary size)
+    cache[tables[1, 0], :, :256] = 0
+    cache[tables[1, 1], :4, :256] = 0
+    out = _prefill(*x, 0.07).cpu()
+    ref, bound = latent_prefill(*x, 0.07)
+    assert_within(out, ref, bound, "prefill")
+    assert (out[200:] == 0).all()
 
 
 @pytest.mark.parametrize("heads,new,old", [
