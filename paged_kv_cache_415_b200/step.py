@@ -89,7 +89,11 @@ class DecodeStep:
         dev = k_cache.device
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=dev) if ws else None
         self.d_status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self._rotated = None              # the rotated queries of steps with a Rotation
+        # The rotated queries of steps with a Rotation.  One buffer of the full
+        # batch (16-bit elements of either type) for the step's whole life: a
+        # captured graph holds its address.
+        self._rotated = torch.empty(num_seqs * num_q_heads * self.head_dim, dtype=torch.int16,
+                                    device=dev)
 
     def __call__(self, query, block_tables, context_lens, scale, out=None, new_key=None,
                  new_value=None, slot_mapping=None, block_mapping=None, stream=None,
@@ -110,15 +114,18 @@ class DecodeStep:
     def _rotate(self, query, new_key, new_value, slot_mapping, positions, rotation, stream):
         """pa_rope_append into the pools; returns the rotated queries, in a
         buffer that the next rotating step reuses."""
-        if self._rotated is None or self._rotated.shape != query.shape \
-                or self._rotated.dtype != query.dtype:
-            self._rotated = torch.empty(query.shape, dtype=query.dtype, device=query.device)
+        if query.dtype not in (torch.float16, torch.bfloat16) \
+                or query.numel() > self._rotated.numel():
+            raise ValueError(f"a step with a rotation takes 16-bit queries of at most "
+                             f"{self.num_seqs} sequences of {self.num_q_heads} heads of "
+                             f"{self.head_dim}, not {query.dtype} {tuple(query.shape)}")
+        rotated = self._rotated[:query.numel()].view(query.dtype).view(query.shape)
         with _range("pa.cache_write"):
-            B.pa_rope_append(self._rotated, query, new_key, new_value, self.k_cache, self.v_cache,
+            B.pa_rope_append(rotated, query, new_key, new_value, self.k_cache, self.v_cache,
                              slot_mapping, positions, rotation.cos_sin, rotation.q_weight,
                              rotation.k_weight, rotation.eps, rotation.interleaved, self.k_scale,
                              self.v_scale, self.k_scales, self.v_scales, self.d_status, stream)
-        return self._rotated
+        return rotated
 
     def _step(self, query, block_tables, context_lens, scale, out, new_key, new_value,
               slot_mapping, block_mapping, stream, max_context_len, fused_append, positions,
@@ -217,6 +224,7 @@ class DecodeStep:
         with torch.cuda.graph(g):
             self(query, block_tables, context_lens, scale,
                  stream=torch.cuda.current_stream(query.device), **args)
+        g.step = self                     # the scratch whose addresses it holds
         return g
 
     def run_from_host(self, host: dict, dev: dict, scale, stream=None, fused_append=False):

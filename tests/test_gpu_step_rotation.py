@@ -1,0 +1,71 @@
+"""Rotating decode steps of several batch sizes through one DecodeStep."""
+import pytest
+import torch
+
+from tests.latent_reference import angle_table
+
+pytestmark = pytest.mark.gpu
+HQ, HKV, D, BLOCK = 8, 2, 128, 16
+
+
+def _batch(seqs, seed, dtype):
+    g = torch.Generator().manual_seed(seed)
+    ctx = torch.tensor([1 + (11 * i) % 40 for i in range(seqs)], dtype=torch.int32)
+    tables = torch.arange(3 * seqs, dtype=torch.int32).view(seqs, 3)
+    p = ctx.long() - 1
+    slots = tables[torch.arange(seqs), p // BLOCK].long() * BLOCK + p % BLOCK
+    x = dict(query=torch.randn(seqs, HQ, D, generator=g).to(dtype),
+             new_key=torch.randn(seqs, HKV, D, generator=g).to(dtype),
+             new_value=torch.randn(seqs, HKV, D, generator=g).to(dtype),
+             block_tables=tables, context_lens=ctx, slot_mapping=slots, positions=p)
+    return {k: v.cuda() for k, v in x.items()}
+
+
+def _want(b, pools, rotation):
+    """Rotate first, then the step on rotated rows, over copies of the pools."""
+    from paged_kv_cache_415_b200 import binding as B
+    from paged_kv_cache_415_b200.step import DecodeStep
+    pools = [p.clone() for p in pools]
+    q = torch.empty_like(b["query"])
+    B.pa_rope_append(q, b["query"], b["new_key"], b["new_value"], *pools, b["slot_mapping"],
+                     b["positions"], rotation.cos_sin)
+    return DecodeStep(*pools, q.shape[0], HQ, 48)(q, b["block_tables"], b["context_lens"], 0.1)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_graphs_of_several_batch_sizes(dtype):
+    """A graph each of two batch sizes, an eager step of a third and tensors
+    allocated in between; replayed in turn with new queries, each gives its
+    own batch's result and no other tensor changes."""
+    from paged_kv_cache_415_b200.step import DecodeStep, Rotation
+    pools = [torch.randn(32, BLOCK, HKV, D, device="cuda").to(dtype) for _ in range(2)]
+    rotation = Rotation(angle_table(64, D).cuda())
+    step = DecodeStep(*pools, 7, HQ, 48)
+    batches = [_batch(s, 10 + s, dtype) for s in (3, 7)]
+    outs, graphs, bystanders = [], [], []
+    others = lambda: [torch.full((n, HQ, D), 5.0, dtype=dtype, device="cuda")
+                      for n in (1, 2, 3, 5, 7) for _ in range(4)]
+    for b in batches:
+        rows = {k: v for k, v in b.items() if k not in ("query", "block_tables", "context_lens")}
+        outs.append(torch.zeros_like(b["query"]))
+        graphs.append(step.graph(b["query"], b["block_tables"], b["context_lens"], 0.1, outs[-1],
+                                 rotation=rotation, **rows))
+        bystanders += others()
+    third = _batch(5, 99, dtype)
+    want = _want(third, pools, rotation)
+    rows = {k: third[k] for k in ("new_key", "new_value", "slot_mapping", "positions")}
+    got = step(third["query"], third["block_tables"], third["context_lens"], 0.1,
+               rotation=rotation, **rows)
+    assert torch.equal(got, want)
+    bystanders += others()
+    assert all(g.step is step for g in graphs)
+    del step
+    bystanders += others()
+    for turn in range(3):
+        for b, out, graph in zip(batches, outs, graphs):
+            b["query"].mul_(-0.75)
+            want = _want(b, pools, rotation)
+            out.zero_()
+            graph.replay()
+            assert torch.equal(out, want), turn
+    assert all((t == 5).all() for t in bystanders)
