@@ -568,6 +568,10 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                         }
                     }
                 }
+                // A segment's last tile: its sums take the place of the maxima,
+                // which every warp has to have read.  (Elsewhere the next tile's
+                // barriers lie between.)
+                if (w.last()) named_barrier(1, 128);
                 // every warp writes the same factors, and reads its own
                 if (lane < 4) {
 #pragma unroll
