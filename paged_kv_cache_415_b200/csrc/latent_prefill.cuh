@@ -449,7 +449,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         }
         __syncthreads();
         item = __shfl_sync(kFullMask, sizes[n], 0);
-        __syncthreads();                                  // (the queries' copies take this place)
+        fence_proxy_async_smem();                         // the queries' copies take this place
+        __syncthreads();
     }
     const int s = item / a.pairs;
     const int row0 = (a.pairs - 1 - item % a.pairs) * 2 * kQueryTile;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests.latent_reference import assert_within, latent_decode
-from tests.test_gpu_latent import _decode, _pool
+from tests.test_gpu_latent import _decode, _pool, _prefill, _prompt
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +30,19 @@ def test_decode_maximum_in_the_last_tile(dtype, heads):
     assert_within(first.cpu(), ref, bound, "decode")
     for _ in range(20):
         assert torch.equal(_decode(query, cache, tables, ctx, 0.05), first)
+
+
+def test_prefill_ranked_blocks_are_those_of_each_sequence_alone():
+    """Blocks taken by size over all sequences (more of them than fit at once)
+    give the bits that each sequence gives by itself, every time."""
+    new, old = [300, 7, 129, 1, 260, 40], [0, 400, 130, 77, 0, 255]
+    x = _prompt(40, 256, 16, new, old, torch.bfloat16, 41)
+    query, cache, w, tables, starts, ctx = x
+    first = _prefill(*x, 192 ** -0.5)
+    for s, n in enumerate(new):
+        a = int(starts[s])
+        alone = _prefill(query[a:a + n], cache, w, tables[s:s + 1].contiguous(),
+                         torch.tensor([0, n], dtype=torch.int32), ctx[s:s + 1], 192 ** -0.5)
+        assert torch.equal(alone, first[a:a + n]), s
+    for _ in range(20):
+        assert torch.equal(_prefill(*x, 192 ** -0.5), first)
