@@ -740,10 +740,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     const bool inside = row < static_cast<int64_t>(a.num_seqs) * a.num_heads;
     const int s = inside ? static_cast<int>(row / a.num_heads) : 0;
     const int h = inside ? static_cast<int>(row % a.num_heads) : 0;
-    // (the decode kernel has let this launch begin: what it read may be read)
+    grid_dependency_wait();
     const int32_t ctx = checked_context(a.context_lens, s, a.max_context_len, a.max_blocks_per_seq,
                                         a.block_size);
-    grid_dependency_wait();
     if (!inside || ctx <= 0) return;
     const int32_t per_cta = a.ws_meta[0];
     const int32_t begin = a.ws_meta[1 + s];

@@ -429,11 +429,23 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         prefetch_tensor_map(&tm_key);
         prefetch_tensor_map(&tm_value);
         prefetch_tensor_map(&tm_rot);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full + i, 1);
+            mbar_init(k_full + i, 1);
+            mbar_init(k_empty + i, 2);                    // both tiles' products
+            mbar_init(v_full + i, 1);
+            mbar_init(v_empty + i, 2);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(s_full + i, 1);
+            mbar_init(p_full + i, 128);
+            mbar_init(pv_done + i, 1);
+        }
+        *begun = 0;
+        fence_barrier_init();
     }
-    // The expansion lets this launch begin once it has seen all earlier work
-    // complete, so what the caller wrote may be read at once; only what the
-    // expansion writes (the workspace) is waited for.  Every block waits before
-    // it ends, so this launch never completes before the expansion.
+    grid_dependency_wait();
+    allow_dependents();
     int32_t item = blockIdx.z * a.pairs + blockIdx.y;
     if (a.sorted) {
         // The item whose size has this block's rank among them all.
@@ -457,12 +469,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     const PromptSpan span = prompt_span(a, s);
     if (threadIdx.x == 0 && h == 0 && row0 == 0 && (span.first < 0 || span.context < 0))
         status_or(a.d_status, PA_STATUS_BAD_CONTEXT);
-    if (row0 >= span.count) {
-        grid_dependency_wait();
-        return;
-    }
+    if (row0 >= span.count) return;
     if (span.context < 0) {                               // zero rows
-        grid_dependency_wait();
         const int n = min(2 * kQueryTile, span.count - row0);
         for (int i = threadIdx.x; i < n * (kValue / 8); i += kAttendThreads) {
             const int64_t row = static_cast<int64_t>(span.first + row0 + i / (kValue / 8)) * a.num_heads + h;
@@ -483,22 +491,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     }
     const int32_t total = max(steps[0], steps[1]);
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(q_full + i, 1);
-            mbar_init(k_full + i, 1);
-            mbar_init(k_empty + i, 2);                    // both tiles' products
-            mbar_init(v_full + i, 1);
-            mbar_init(v_empty + i, 2);
-        }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(s_full + i, 1);
-            mbar_init(p_full + i, 128);
-            mbar_init(pv_done + i, 1);
-        }
-        *begun = 0;
-        fence_barrier_init();
-    }
     if (warp == 9) tmem_alloc(tmem_slot, 512);
     tmem_fence_before();
     __syncthreads();
@@ -517,8 +509,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                             span.first + row0 + t * kQueryTile, h, q_full + t);
         };
         queries(0);                                       // the second tile's after the first keys
-        grid_dependency_wait();
-        allow_dependents();
         int32_t keys = 0, values = 0;                     // tiles copied
         const int32_t plane = s * a.num_heads + h;
         for (int32_t i = 0; i < total; ++i) {
@@ -646,7 +636,6 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + quarter + t * kKvTile;
         const uint32_t o_tmem = tmem + quarter + S::kOCol + t * kValue;
-        grid_dependency_wait();                           // the masks are the expansion's
         float m = -INFINITY, l = 0.f;
         for (int32_t j = 0; j < 2 * n; ++j) {
             const int half = j & 1;

@@ -3,7 +3,7 @@ hardest: maxima that move late, values of far powers of two, long pipelines."""
 import pytest
 import torch
 
-from tests.latent_reference import assert_within, latent_decode
+from tests.latent_reference import assert_within, latent_decode, latent_prefill
 from tests.test_gpu_latent import _decode, _pool, _prefill, _prompt
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +46,46 @@ def test_prefill_ranked_blocks_are_those_of_each_sequence_alone():
         assert torch.equal(alone, first[a:a + n]), s
     for _ in range(20):
         assert torch.equal(_prefill(*x, 192 ** -0.5), first)
+
+
+def test_lengths_written_right_before_the_call():
+    """Lengths, starts and queries that the work just before on the stream
+    writes: every call follows its own, with nothing waited for between."""
+    from paged_kv_cache_415_b200 import binding as B
+    a = [t.cuda() for t in _prompt(6, 256, 16, [90, 200, 3], [40, 0, 300], torch.float16, 51)]
+    b = [t.cuda() for t in _prompt(6, 256, 16, [150, 1, 142], [0, 330, 20], torch.float16, 52)]
+    query, cache, w, tables, starts, ctx = (torch.empty_like(x) for x in a)
+    width = max(a[3].shape[1], b[3].shape[1])
+    blocks = max(a[1].shape[0], b[1].shape[0])
+    cache = torch.zeros(blocks, *a[1].shape[1:], dtype=torch.float16, device="cuda")
+    tables = torch.zeros(3, width, dtype=torch.int32, device="cuda")
+    absorbed = [torch.randn(3, 6, 320, device="cuda").half() for _ in range(2)]
+    n = B.pa_latent_prefill_workspace_size(3, 6, 256, 16, 340)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    n = B.pa_latent_decode_workspace_size(3, 6, 256, 16, 340)
+    ws_d = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
+
+    def take(x, q):
+        query.copy_(x[0])
+        cache[:x[1].shape[0]].copy_(x[1])
+        w.copy_(x[2])
+        tables.zero_()
+        tables[:, :x[3].shape[1]].copy_(x[3])
+        starts.copy_(x[4])
+        ctx.copy_(x[5])
+        out = torch.empty(293, 6, 128, dtype=torch.float16, device="cuda")
+        B.pa_latent_prefill(out, query, cache, w, tables, starts, ctx, 200, 340, 0.07, ws)
+        dec = torch.empty(3, 6, 256, dtype=torch.float16, device="cuda")
+        B.pa_latent_decode(dec, q, cache, tables, ctx, 340, 0.05, workspace=ws_d)
+        return out, dec
+
+    want = []
+    for x, q in zip((a, b), absorbed):
+        got = take(x, q)
+        torch.cuda.synchronize()
+        ref, bound = latent_prefill(*(t.cpu() for t in x), 0.07)
+        assert_within(got[0].cpu(), ref, bound, "prefill")
+        want.append(got)
+    got = [take(x, q) for _ in range(30) for x, q in zip((a, b), absorbed)]
+    for i, pair in enumerate(got):
+        assert all(torch.equal(g, r) for g, r in zip(pair, want[i % 2])), i
