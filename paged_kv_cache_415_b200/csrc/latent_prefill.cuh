@@ -361,6 +361,7 @@ struct AttendShape {
 
 constexpr int kAttendThreads = 352;
 constexpr int kHalf = kKvTile / 2;              // keys whose scores and weights are under way at once
+constexpr float kFaint = -40.0f;                // log2 of products of no account
 constexpr int kSortItems = 128;                 // pairs of query tiles at most that are sorted
 
 // How long pair `item` of the query tiles takes, about: a step of both tiles
@@ -671,35 +672,51 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                     max3(top[(e >> 1 & 1) + 2 * (e >> 5)], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
             // Weights take the powers of two of their values along: w = 2^(x + ex - m),
             // so m follows the largest product of a weight and a value, and
-            //   out = sum w V' / sum w 2^-ex.
-            const float peak = fmaxf(fmaf(fmaxf(top[0], top[1]), unit, ex.x),
-                                     fmaf(fmaxf(top[2], top[3]), unit, ex.y));
-            // The reference moves where it is unset or passed by 2^8.
+            //   out = sum w V' / l,  l = sum w 2^-ex = sum 2^(x - m).
+            const float peaks[2] = {fmaf(fmaxf(top[0], top[1]), unit, ex.x),
+                                    fmaf(fmaxf(top[2], top[3]), unit, ex.y)};
+            const float peak = fmaxf(peaks[0], peaks[1]);
+            // The reference moves where it is unset or passed by 2^8.  32 tokens whose
+            // products all lie 2^-40 below it are faint: their weights are 0 in fp16, but
+            // in l they count (zeros beside values of 2^70).  2^(x + ex - m) may be below
+            // what fp32 has, 2^(x - m) is not where it matters, so they go without ex.
             const bool moves = peak > m + 8.0f;
-            if (__any_sync(kFullMask, moves)) {
-                const float f = moves ? exp2_fast(m - peak) : 1.f;
-                if (moves) m = peak;
-                l *= f;
-                if (j > 0) {
-                    ok = mbar_poll_warp(pv_done + 2 * t + (half ^ 1), ((j - 1) >> 1) & 1);
-                    if (!ok) break;
-                    tmem_fence_after();
+            bool faint[2] = {false, false}, any_faint = false;
+            if (__any_sync(kFullMask, moves || fminf(peaks[0], peaks[1]) < m + kFaint)) {
+                if (__any_sync(kFullMask, moves)) {
+                    const float f = moves ? exp2_fast(m - peak) : 1.f;
+                    // l may be held by tokens of small values: its factor, 2^-186 at the
+                    // least for equal scores, is applied as two that fp32 has
+                    const float root = moves ? exp2_fast(0.5f * (m - peak)) : 1.f;
+                    if (moves) m = peak;
+                    l = l * root * root;
+                    if (j > 0) {
+                        ok = mbar_poll_warp(pv_done + 2 * t + (half ^ 1), ((j - 1) >> 1) & 1);
+                        if (!ok) break;
+                        tmem_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < kValue; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o, o_tmem + c);
-                        tmem_wait_ld();
+                        for (int c = 0; c < kValue; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(o, o_tmem + c);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(o_tmem + c, o);
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(o_tmem + c, o);
+                        }
+                        tmem_wait_st();
                     }
-                    tmem_wait_st();
                 }
+                faint[0] = peaks[0] < m + kFaint;
+                faint[1] = peaks[1] < m + kFaint;
+                any_faint = __any_sync(kFullMask, faint[0] || faint[1]);
             }
             const float sub = m == -INFINITY ? 0.f : m;
+            const float shift[2] = {faint[0] ? 0.f : ex.x, faint[1] ? 0.f : ex.y};
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 unit2 = make_float2(unit, unit);
-            const float2 add[2] = {make_float2(ex.x - sub, ex.x - sub), make_float2(ex.y - sub, ex.y - sub)};
+            const float2 add[2] = {make_float2(shift[0] - sub, shift[0] - sub),
+                                   make_float2(shift[1] - sub, shift[1] - sub)};
             uint32_t p[kHalf / 2];
 #pragma unroll
             for (int e = 0; e < kHalf / 2; ++e) {
@@ -709,8 +726,12 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 sum[e >> 4] = add2(sum[e >> 4], w);
                 p[e] = Elem<__half>::from_float2(w.x, w.y);
             }
+            if (any_faint) {
+#pragma unroll
+                for (int e = 0; e < kHalf / 2; ++e) p[e] = faint[e >> 4] ? 0u : p[e];
+            }
             tmem_st32(s_tmem + half * kHalf, p);
-            l += (sum[0].x + sum[0].y) * exp2_fast(-ex.x) + (sum[1].x + sum[1].y) * exp2_fast(-ex.y);
+            l += (sum[0].x + sum[0].y) * exp2_fast(-shift[0]) + (sum[1].x + sum[1].y) * exp2_fast(-shift[1]);
             tmem_wait_st();
             tmem_fence_before();
             mbar_arrive(p_full + 2 * t + half);
@@ -719,7 +740,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
         if (ok && n > 0) ok = mbar_poll_warp(pv_done + 2 * t + 1, (n - 1) & 1);
         if (ok && n > 0) {
             tmem_fence_after();
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;      // (NaN where a score was)
             // Through shared memory (the tile's queries have been used), 8 KB a
             // warp: stored a row a thread, the 32 lines that each store touches
             // took 9000 cycles.  16-byte chunk j of row r lies at j ^ (r % 8).

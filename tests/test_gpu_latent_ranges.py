@@ -3,7 +3,7 @@ hardest: maxima that move late, values of far powers of two, long pipelines."""
 import pytest
 import torch
 
-from tests.latent_reference import assert_within, latent_decode, latent_prefill
+from tests.latent_reference import F64, assert_within, latent_decode, latent_prefill
 from tests.test_gpu_latent import _decode, _pool, _prefill, _prompt
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +89,46 @@ def test_lengths_written_right_before_the_call():
     got = [take(x, q) for _ in range(30) for x, q in zip((a, b), absorbed)]
     for i, pair in enumerate(got):
         assert all(torch.equal(g, r) for g, r in zip(pair, want[i % 2])), i
+
+
+def _far_powers(powers, dtype, seed, new=70, old=90):
+    """A prompt whose tokens' latent vectors are scaled by 2^powers[g], g the
+    token's group of 32 (None: zeros); keys take the rotated part alone."""
+    x = _prompt(2, 256, 16, [new], [old], dtype, seed)
+    query, cache, w, tables, starts, ctx = x
+    w[:, :128] = 0
+    t = torch.arange(new + old)
+    power = torch.tensor([-1000.0 if p is None else p for p in powers])[t // 32]
+    rows = cache[tables[0][t // 16].long(), t % 16]
+    rows[:, :256] = (rows[:, :256].to(F64) * torch.exp2(power.to(F64))[:, None]).to(dtype)
+    cache[tables[0][t // 16].long(), t % 16] = rows
+    return x
+
+
+@pytest.mark.parametrize("powers", [
+    (None, 70, None, None, 70), (70, None, None, 70, None), (None, None, None, None, 115),
+    (110, None, None, None, None), (-55, 10, 70, None, 40), (70, 40, 10, -20, -55),
+    (None, -50, None, 0, 90),
+])
+def test_prefill_values_of_far_powers(powers):
+    """Groups of 32 tokens whose values lie up to 2^170 apart, zeros among
+    them: every token counts in the sum of the weights."""
+    x = _far_powers(powers, torch.bfloat16, 61)
+    out = _prefill(*x, 0.05)
+    ref, bound = latent_prefill(*x, 0.05)
+    assert_within(out.cpu(), ref, bound, f"powers {powers}")
+
+
+@pytest.mark.parametrize("lean", [-1, 1])
+def test_prefill_far_powers_against_the_scores(lean):
+    """Values of 2^60 whose tokens score 100 powers of two lower or higher
+    than those of ordinary values."""
+    x = _far_powers((0, 60, 0, 60, 0), torch.bfloat16, 62)
+    query, cache, w, tables, starts, ctx = x
+    query[..., -1] = 8.0
+    t = torch.arange(160)
+    lift = torch.where((t // 32) % 2 == 1, lean * 100 * 0.6931 / (0.05 * 8.0), 0.0)
+    cache[tables[0][t // 16].long(), t % 16, -1] = lift.bfloat16()
+    out = _prefill(*x, 0.05)
+    ref, bound = latent_prefill(*x, 0.05)
+    assert_within(out.cpu(), ref, bound, f"lean {lean}")
