@@ -705,6 +705,8 @@ PA_API pa_status pa_latent_append(
  *                aligned (may be NULL when that is 0); its contents on entry
  *                do not matter; calls that share it must not overlap.
  * Products take 16-bit operands with fp32 sums; softmax statistics are fp32.
+ * Weights are rounded to `dtype`; F16 weights 2^-21 of a run of tiles' first
+ * or largest keep fewer bits, at 2^-32 none.
  * Other arguments, empty and bad contexts, bad blocks, the order of sums and
  * status bits as pa_paged_decode.
  */
@@ -730,8 +732,11 @@ PA_API pa_status pa_latent_decode(void* out, const void* query, const void* cach
  *   out = sum_t softmax(x)_t V_t.
  * A query that sees a token of which some element of V is not finite gives NaN
  * in that head; queries before the token do not meet it.  K is rounded to
- * `dtype`, V to fp16 with a power of two a head and 32 tokens (any finite V has
- * a place, elements 2^-14 of the largest of the 32 keep fewer bits).
+ * `dtype`.  V is kept in fp16 with a power of two a head and 32 tokens: any
+ * finite V of 2^-74 or more has a place, elements 2^-14 of the largest of the 32
+ * keep fewer bits.  Weights are kept in fp16: where a weight times that largest V is
+ * 2^-21 of the row's largest such product it keeps fewer bits, at 2^-32 none; the
+ * sum that normalises them is fp32 and has them all.
  *
  * out            [num_tokens][num_heads][value_dim], 16-byte aligned; written
  *                for the rows of the sequences, others are left as they were.

@@ -28,6 +28,8 @@
 // head and takes p = 2^(x - m) at once; only if some x passes m by more than 8
 // (or m is not set yet) do the warps put their maxima together, move m and
 // rescale O^T.  So p <= 2^8, exact in 16 bits up to the rounding every p has.
+// For fp16, whose smallest numbers are near, m lies another 2^7 lower: p <= 2^15,
+// and weights down to 2^-21 of the reference keep all their bits (2^-14 without).
 //
 // Measured: 256 sequences of 3500 to 4500 tokens, 16 heads, in 204.7 us of this
 // kernel (1.20 GB, 5.9 TB/s: memory); 64 sequences to 4096 tokens, 128 heads,
@@ -49,7 +51,13 @@ constexpr int kTile = 64;                       // tokens of a tile
 constexpr int kLatentThreads = 256;
 constexpr int kMaxGroupHeads = 64;              // heads a CTA serves
 constexpr int kAhead = 3;                       // tiles whose pages are looked up ahead
-constexpr float kRescaleAbove = 8.0f;           // log2 of how far p may pass 1
+constexpr float kRescaleAbove = 8.0f;           // log2 of how far p may pass the reference's
+// log2 of the reference token's own p: up to 2^15 fit into fp16, bf16 has the
+// exponents of fp32
+template <typename T>
+constexpr float kHeadroom = 0.0f;
+template <>
+constexpr float kHeadroom<__half> = 7.0f;
 
 struct LatentDecodeArgs {
     void* out;
@@ -513,8 +521,8 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
 #pragma unroll
                 for (int k = 0; k < J; ++k) {
                     const float2 v = *reinterpret_cast<const float2*>(tops + 8 * k + head0);
-                    if (8 * k + head0 < heads) m[2 * k] = fmaxf(v.x, -FLT_MAX);
-                    if (8 * k + head0 + 1 < heads) m[2 * k + 1] = fmaxf(v.y, -FLT_MAX);
+                    if (8 * k + head0 < heads) m[2 * k] = fmaxf(v.x, -FLT_MAX) - kHeadroom<T>;
+                    if (8 * k + head0 + 1 < heads) m[2 * k + 1] = fmaxf(v.y, -FLT_MAX) - kHeadroom<T>;
                 }
             }
             float y[4 * J];
@@ -529,7 +537,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             float high[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 4 * J; ++i) high[i & 1] = fmaxf(high[i & 1], y[i]);
-            const bool move = named_barrier_or(1, 128, fmaxf(high[0], high[1]) > kRescaleAbove);
+            const bool move = named_barrier_or(1, 128, fmaxf(high[0], high[1]) > kRescaleAbove + kHeadroom<T>);
             if (move) {
                 // Maxima of the tile: over the lane's tokens, the warp's, the warps'.
 #pragma unroll
@@ -559,7 +567,7 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float t = e ? top.y : top.x;
+                        const float t = (e ? top.y : top.x) - kHeadroom<T>;
                         f[2 * k + e] = 1.f;
                         if (t > m[2 * k + e] + kRescaleAbove) {   // (never past the heads)
                             f[2 * k + e] = exp2_fast(m[2 * k + e] - t);

@@ -23,7 +23,11 @@
 // added as much error each as the output's own rounding (0.0027 of the output
 // in all, its own 0.0017; with fp16 0.0020, for 1 % of the time), and no finite
 // value passes the type.  A token whose values are 2^14 below the largest of its
-// 32 begins to lose bits.
+// 32 begins to lose bits.  So does a weight whose product with that largest value is
+// 2^21 below the row's largest such product; below 2^32 it is gone from the output
+// (not from the weights' sum).  Long prompts have such: a first token that takes
+// most of the mass and has a small value.  With weights of at most 2^8, not 2^15,
+// those bounds were 2^14 and 2^25: at 32768 tokens and 2^24 a weight 4 % of the output.
 #pragma once
 
 #include <cuda.h>
@@ -362,6 +366,7 @@ struct AttendShape {
 constexpr int kAttendThreads = 352;
 constexpr int kHalf = kKvTile / 2;              // keys whose scores and weights are under way at once
 constexpr float kFaint = -40.0f;                // log2 of products of no account
+constexpr float kHeadroom = 7.0f;               // weights are kept times 2^7, up to 2^15: what fp16 has room for
 constexpr int kSortItems = 128;                 // pairs of query tiles at most that are sorted
 
 // How long pair `item` of the query tiles takes, about: a step of both tiles
@@ -711,7 +716,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
                 faint[1] = peaks[1] < m + kFaint;
                 any_faint = __any_sync(kFullMask, faint[0] || faint[1]);
             }
-            const float sub = m == -INFINITY ? 0.f : m;
+            const float sub = (m == -INFINITY ? 0.f : m) - kHeadroom;
             const float shift[2] = {faint[0] ? 0.f : ex.x, faint[1] ? 0.f : ex.y};
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 unit2 = make_float2(unit, unit);

@@ -132,3 +132,75 @@ def test_prefill_far_powers_against_the_scores(lean):
     out = _prefill(*x, 0.05)
     ref, bound = latent_prefill(*x, 0.05)
     assert_within(out.cpu(), ref, bound, f"lean {lean}")
+
+
+def _leader(ctx, gap, lat, dtype, seed):
+    """A context whose first token outweighs each other one by about 2^gap and
+    has the value 0, so that the output is made of the faint ones alone.
+    Scores come from one element of the rotated part: 8 r scale, exact but for
+    the scale's rounding.  Returns (cache, tables, rows, p [ctx], total)."""
+    g = torch.Generator().manual_seed(seed)
+    cache, tables = _pool([ctx], 16, lat, dtype, g)
+    t = torch.arange(ctx)
+    rows = (torch.randn(ctx, lat + 64, generator=g) * 0.25).abs().to(dtype)
+    rows[:, lat:] = 0
+    rows[:, -1] = (torch.rand(ctx, generator=g) - 0.5).to(dtype)
+    rows[0] = 0
+    rows[0, -1] = gap
+    cache[tables[0][t // 16].long(), t % 16] = rows
+    p = torch.exp2(rows[:, -1].to(F64) - gap)
+    return cache, tables, rows.to(F64), p, p.sum()
+
+
+_EIGHTH = 0.6931471805599453 / 8                     # 8 r scale = r ln 2
+# What is left to err: the scale in fp32 and the references (at most 64 * 2^-23
+# together in the exponent), 2^-22 of an exponential, fp32 sums of t terms.
+_SLACK = 64 * 2.0 ** -23 + 2.0 ** -22
+
+
+@pytest.mark.parametrize("gap", [10, 20, 24])
+@pytest.mark.parametrize("ctx", [1000, 32768])
+def test_decode_faint_weights(ctx, gap):
+    """fp16 weights: 2^7 of room above the reference is used, so a weight is
+    off by 2^-11 of itself or by 2^-32 of the leader's."""
+    lat = 256
+    cache, tables, rows, p, total = _leader(ctx, gap, lat, torch.float16, gap)
+    query = torch.zeros(1, 3, lat + 64, dtype=torch.float16)
+    query[..., -1] = 8
+    out = _decode(query, cache, tables, torch.tensor([ctx], dtype=torch.int32), _EIGHTH)
+    values = rows[:, :lat]
+    ref = (p @ values) / total
+    off = torch.clamp(p * 2.0 ** -11, min=2.0 ** -32)
+    bound = (off @ values) / total + (_SLACK + (ctx + 8) * 2.0 ** -23) * ref
+    bound = bound + 2.0 ** -11 * (ref + bound) + 2.0 ** -25
+    assert_within(out.cpu()[0], ref.expand(3, -1), bound.expand(3, -1), f"gap {gap}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("gap", [10, 20, 24])
+def test_prefill_faint_weights(dtype, gap):
+    """The same in the prompt's attention, whose weights are fp16 for both
+    types; its values too, off by 2^-11 of themselves (the expansion here
+    takes one element of the row: no sum)."""
+    ctx, lat, new = 20000, 256, 3
+    cache, tables, rows, p, _ = _leader(ctx, gap, lat, dtype, gap)
+    u = 2.0 ** -11 if dtype == torch.float16 else 2.0 ** -8
+    query = torch.zeros(new, 2, 192, dtype=dtype)
+    query[..., -1] = 8
+    w = torch.zeros(2, 256, lat, dtype=dtype)
+    e = torch.arange(128)
+    w[:, 128 + e, e] = 1
+    out = _prefill(query, cache, w, tables, torch.tensor([0, new], dtype=torch.int32),
+                   torch.tensor([ctx], dtype=torch.int32), _EIGHTH).cpu()
+    for i in range(new):
+        n = ctx - new + 1 + i
+        values = rows[:n, :128]
+        ref = (p[:n] @ values) / p[:n].sum()
+        # a weight is taken times its 32 tokens' power of two, which is 1 or 2 here
+        # (their largest value lies in [0.5, 2)), so may be half as fine as the leader's
+        assert all(0.5 <= float(v.amax()) < 2 for v in values.split(32) if len(v) == 32)
+        off = torch.clamp(p[:n] * 2.0 ** -11, min=2.0 ** -31)
+        bound = (off @ values) / p[:n].sum() \
+            + (_SLACK + 2.0 ** -11 + (n + 8) * 2.0 ** -23) * ref
+        bound = bound + u * (ref + bound) + 2.0 ** -25
+        assert_within(out[i], ref.expand(2, -1), bound.expand(2, -1), f"gap {gap}")
