@@ -486,10 +486,12 @@ __global__ void __launch_bounds__(kLatentThreads, 1)
             const uint64_t mask = masks[st];
             const bool whole = mask == ~0ull;
             if (fresh) {
-                // columns past the heads: p = 0, and their reference never moves
+                // Unset, a reference is the least finite value: any score passes it but
+                // -inf, which less it is still -inf.  Columns past the heads: p = 0, and
+                // their reference never moves.
 #pragma unroll
                 for (int i = 0; i < 2 * J; ++i) {
-                    m[i] = 8 * (i >> 1) + head0 + (i & 1) < heads ? -INFINITY : INFINITY;
+                    m[i] = 8 * (i >> 1) + head0 + (i & 1) < heads ? -FLT_MAX : INFINITY;
                     l[i] = 0.f;
                 }
             }

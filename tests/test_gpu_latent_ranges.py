@@ -3,7 +3,8 @@ hardest: maxima that move late, values of far powers of two, long pipelines."""
 import pytest
 import torch
 
-from tests.latent_reference import F64, assert_within, latent_decode, latent_prefill
+from tests.latent_reference import (F64, assert_within, attend, context_rows, latent_decode,
+                                    latent_prefill)
 from tests.test_gpu_latent import _decode, _pool, _prefill, _prompt
 
 pytestmark = pytest.mark.gpu
@@ -204,3 +205,24 @@ def test_prefill_faint_weights(dtype, gap):
             + (_SLACK + 2.0 ** -11 + (n + 8) * 2.0 ** -23) * ref
         bound = bound + u * (ref + bound) + 2.0 ** -25
         assert_within(out[i], ref.expand(2, -1), bound.expand(2, -1), f"gap {gap}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("finite", [1, 30, 200])
+def test_decode_minus_infinity_behind_bad_blocks(dtype, finite):
+    """A tile of bad blocks, then a tile whose scores are all minus infinity:
+    neither weighs anything, what follows is as it is alone."""
+    ctx, lat = 128 + finite, 256
+    g = torch.Generator().manual_seed(finite)
+    cache, tables = _pool([ctx], 16, lat, dtype, g)
+    query = torch.randn(1, 16, lat + 64, generator=g).to(dtype)
+    query[..., lat] = query[..., lat].abs() + 0.5
+    t = torch.arange(64, 128)
+    cache[tables[0][t // 16].long(), t % 16, lat] = 0
+    rows, _ = context_rows(cache, tables[0], ctx)
+    seen = (torch.arange(ctx) >= 128).expand(16, ctx)
+    ref, bound = attend(query[0].to(F64), rows, rows[:, :lat], seen, 0.05, dtype)
+    cache[tables[0][t // 16].long(), t % 16, lat] = -float("inf")
+    tables[0, :4] = -1
+    out = _decode(query, cache, tables, torch.tensor([ctx], dtype=torch.int32), 0.05)
+    assert_within(out.cpu()[0], ref, bound, "decode")
