@@ -13,6 +13,7 @@ tensor (bits PA_STATUS_*).
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 import torch
@@ -150,8 +151,6 @@ def _load() -> ctypes.CDLL:
 
 
 LIB = _load()
-
-from . import _marshal  # noqa: E402  (built beside libpa.so; no fallback)
 
 
 def _ptr(t) -> int | None:
@@ -523,15 +522,32 @@ def pa_swap_blocks(src_k, src_v, dst_k, dst_v, block_mapping, d_status=None, str
 # refused with ValueError, before the C call: in _marshal (csrc_py/marshal.cpp),
 # where that costs well under a microsecond.  The device of the tensors is made
 # current for the call; without a stream it goes to that device's current one.
+# _marshal is loaded with the first of these calls, and has to have been built
+# for this torch; the other calls need libpa.so alone.  There is no fallback.
 # ---------------------------------------------------------------------------
 
-def _bind_marshal(lib):
-    address = lambda name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
-    _marshal.bind(address("pa_rope_append"), address("pa_latent_append"),
-                  address("pa_latent_decode"), address("pa_latent_prefill"))
+class _Marshal:
+    """The functions of _marshal.so, loaded when the first is asked for."""
+
+    def __getattr__(self, name):
+        try:
+            module = importlib.import_module("._marshal", __package__)
+        except ImportError as e:
+            raise ImportError(f"_marshal.so is not built for this torch and Python ({e}): run "
+                              "`python -m paged_kv_cache_415_b200.build`") from e
+        built_for = getattr(module, "torch_version", "another")
+        if built_for != torch.__version__:
+            raise ImportError(f"_marshal.so was built for torch {built_for}, this is "
+                              f"{torch.__version__}: run `python -m paged_kv_cache_415_b200.build`")
+        module.bind(*(ctypes.cast(getattr(LIB, f), ctypes.c_void_p).value
+                      for f in ("pa_rope_append", "pa_latent_append", "pa_latent_decode",
+                                "pa_latent_prefill")))
+        for f in ("rope_append", "latent_append", "latent_decode", "latent_prefill"):
+            setattr(self, f, getattr(module, f))
+        return object.__getattribute__(self, name)
 
 
-_bind_marshal(LIB)
+_marshal = _Marshal()
 
 
 def pa_rope_append(query_out, query, key, value, k_cache, v_cache, slot_mapping, positions,

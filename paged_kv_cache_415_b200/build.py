@@ -26,6 +26,7 @@ LIB = os.path.join(HERE, "libpa.so")
 MARSHAL_SOURCE = os.path.join(HERE, "csrc_py", "marshal.cpp")
 MARSHAL = os.path.join(HERE, "_marshal.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
+MARSHAL_KEY = os.path.join(BUILD_DIR, "_marshal.key")      # what _marshal.so was built for
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -61,22 +62,31 @@ def _newer(target, deps) -> bool:
     return all(os.path.getmtime(p) <= t for p in deps)
 
 
+def _read(path) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
+
+
 def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
 def build_marshal(force: bool = False) -> str:
-    """_marshal.so, a CPython extension over torch's tensors."""
-    deps = [MARSHAL_SOURCE, os.path.join(INCLUDE, "pa.h"), os.path.abspath(__file__)]
-    if not force and _newer(MARSHAL, deps):
-        return MARSHAL
+    """_marshal.so, a CPython extension over torch's tensors.  Built anew as
+    well when Python or torch is another one than it was built for."""
     import torch
+    built_for = f"{sys.implementation.cache_tag} torch {torch.__version__}"
+    deps = [MARSHAL_SOURCE, os.path.join(INCLUDE, "pa.h"), os.path.abspath(__file__)]
+    if not force and _newer(MARSHAL, deps) and _read(MARSHAL_KEY) == built_for:
+        return MARSHAL
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     root = os.path.dirname(torch.__file__)
     lib, inc = os.path.join(root, "lib"), os.path.join(root, "include")
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-fvisibility=hidden", f'-DPA_TORCH_VERSION="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(cuda, "include"),
            "-isystem" + inc, "-isystem" + os.path.join(inc, "torch", "csrc", "api", "include"),
            MARSHAL_SOURCE, "-o", tmp, "-L" + lib,
@@ -85,6 +95,9 @@ def build_marshal(force: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on {MARSHAL_SOURCE}:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, MARSHAL)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(MARSHAL_KEY, "w") as f:
+        f.write(built_for)
     return MARSHAL
 
 

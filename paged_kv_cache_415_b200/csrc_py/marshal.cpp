@@ -350,4 +350,19 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "argument marshalling f
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal(void) { return PyModule_Create(&module); }
+// The file's name carries no version, so it says for itself what it was built
+// for: the torch as an attribute, the Python here.
+PyMODINIT_FUNC PyInit__marshal(void)
+{
+    const std::string built = std::to_string(PY_MAJOR_VERSION) + "." + std::to_string(PY_MINOR_VERSION) + ".";
+    if (std::string(Py_GetVersion()).compare(0, built.size(), built) != 0) {
+        PyErr_Format(PyExc_ImportError, "built for Python %sx", built.c_str());
+        return nullptr;
+    }
+    PyObject* m = PyModule_Create(&module);
+    if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", PA_TORCH_VERSION) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
