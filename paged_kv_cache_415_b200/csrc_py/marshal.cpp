@@ -102,6 +102,21 @@ bool vector_of(const at::Tensor& t, int64_t n, at::ScalarType type)
     return t.scalar_type() == type && t.dim() == 1 && t.size(0) == n && t.is_contiguous();
 }
 
+// The C calls run without the interpreter's lock, as through ctypes: other
+// threads go on while a launch waits for the driver.  The arguments stay alive,
+// their caller holds them.
+struct Unlocked {
+    PyThreadState* const state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+template <typename F, typename... Args>
+int call_unlocked(F f, Args... args)
+{
+    const Unlocked unlocked;
+    return f(args...);
+}
+
 // The device that all the tensors are on, made current for the call.
 struct OnDevice {
     c10::cuda::CUDAGuard guard;
@@ -167,8 +182,8 @@ int rope_append(PyObject* const* a)
     const OnDevice on(one_device(fn, query, &query_out, &key, &value, &k_cache, &v_cache, &slots, &pos, &table,
                                  qw, kw, ks, vs, status),
                       whole(a[18]));
-    return g_rope_append(
-        ptr(&query_out), ptr(&query), ptr(&key), ptr(&value), ptr(&k_cache), ptr(&v_cache),
+    return call_unlocked(
+        g_rope_append, ptr(&query_out), ptr(&query), ptr(&key), ptr(&value), ptr(&k_cache), ptr(&v_cache),
         static_cast<float*>(ptr(ks)), static_cast<float*>(ptr(vs)), static_cast<int64_t*>(ptr(&slots)),
         static_cast<int64_t*>(ptr(&pos)), static_cast<float*>(ptr(&table)), ptr(qw), ptr(kw),
         static_cast<float>(eps), narrow(tokens), narrow(hq), narrow(hkv), narrow(d), narrow(table.size(1)),
@@ -218,8 +233,8 @@ int latent_append(PyObject* const* a)
     check_status(fn, status);
     const OnDevice on(one_device(fn, cache, q_out, q_in, &latent, &slots, &pos, &table, weight, status),
                       whole(a[11]));
-    return g_latent_append(
-        ptr(q_out), ptr(q_in), ptr(&latent), ptr(&cache), static_cast<int64_t*>(ptr(&slots)),
+    return call_unlocked(
+        g_latent_append, ptr(q_out), ptr(q_in), ptr(&latent), ptr(&cache), static_cast<int64_t*>(ptr(&slots)),
         static_cast<int64_t*>(ptr(&pos)), static_cast<float*>(ptr(&table)), ptr(weight),
         static_cast<float>(eps), narrow(tokens), narrow(heads), narrow(width - rope), narrow(rope),
         table.size(0), pairs ? 1 : 0, o_t, o_h, q_t, q_h, latent.stride(0), narrow(cache.size(1)),
@@ -257,12 +272,12 @@ int latent_decode(PyObject* const* a)
     need(fn, ws == nullptr || ws->is_contiguous(), "workspace must be contiguous");
     check_status(fn, status);
     const OnDevice on(one_device(fn, query, &out, &cache, &tables, &lens, ws, status), whole(a[9]));
-    return g_latent_decode(ptr(&out), ptr(&query), ptr(&cache), static_cast<int32_t*>(ptr(&tables)),
-                           static_cast<int32_t*>(ptr(&lens)), narrow(seqs), narrow(query.size(1)),
-                           narrow(lat), narrow(query.size(2) - lat), narrow(cache.size(1)),
-                           narrow(tables.size(1)), cache.size(0), narrow(max_context),
-                           static_cast<float>(scale), ptr(ws), bytes(ws), type_code(query.scalar_type()),
-                           static_cast<int32_t*>(ptr(status)), on.stream);
+    return call_unlocked(
+        g_latent_decode, ptr(&out), ptr(&query), ptr(&cache), static_cast<int32_t*>(ptr(&tables)),
+        static_cast<int32_t*>(ptr(&lens)), narrow(seqs), narrow(query.size(1)), narrow(lat),
+        narrow(query.size(2) - lat), narrow(cache.size(1)), narrow(tables.size(1)), cache.size(0),
+        narrow(max_context), static_cast<float>(scale), ptr(ws), bytes(ws), type_code(query.scalar_type()),
+        static_cast<int32_t*>(ptr(status)), on.stream);
 }
 
 int latent_prefill(PyObject* const* a)
@@ -291,13 +306,14 @@ int latent_prefill(PyObject* const* a)
     check_status(fn, status);
     const OnDevice on(one_device(fn, query, &out, &cache, &w, &tables, &starts, &lens, ws, status),
                       whole(a[12]));
-    return g_latent_prefill(ptr(&out), ptr(&query), ptr(&cache), ptr(&w), static_cast<int32_t*>(ptr(&tables)),
-                            static_cast<int32_t*>(ptr(&starts)), static_cast<int32_t*>(ptr(&lens)),
-                            narrow(seqs), narrow(query.size(0)), narrow(query.size(1)), narrow(lat),
-                            narrow(rope), narrow(nope), narrow(value), narrow(cache.size(1)),
-                            narrow(tables.size(1)), cache.size(0), narrow(max_query), narrow(max_context),
-                            static_cast<float>(scale), ptr(ws), bytes(ws), type_code(type),
-                            static_cast<int32_t*>(ptr(status)), on.stream);
+    return call_unlocked(
+        g_latent_prefill, ptr(&out), ptr(&query), ptr(&cache), ptr(&w),
+        static_cast<int32_t*>(ptr(&tables)), static_cast<int32_t*>(ptr(&starts)),
+        static_cast<int32_t*>(ptr(&lens)), narrow(seqs), narrow(query.size(0)), narrow(query.size(1)),
+        narrow(lat), narrow(rope), narrow(nope), narrow(value), narrow(cache.size(1)),
+        narrow(tables.size(1)), cache.size(0), narrow(max_query), narrow(max_context),
+        static_cast<float>(scale), ptr(ws), bytes(ws), type_code(type), static_cast<int32_t*>(ptr(status)),
+        on.stream);
 }
 
 template <int (*call)(PyObject* const*), Py_ssize_t N>
