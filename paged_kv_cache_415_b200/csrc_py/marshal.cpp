@@ -68,6 +68,16 @@ int64_t whole(PyObject* o)
     return v;
 }
 
+bool truth(PyObject* o, const char* name)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) {                          // (an array of several elements)
+        PyErr_Clear();
+        throw Refused(std::string(name) + " is neither true nor false");
+    }
+    return v != 0;
+}
+
 // Sizes that the C call takes as int32.
 int32_t narrow(int64_t v)
 {
@@ -152,7 +162,7 @@ int rope_append(PyObject* const* a)
                      &table = *tensor(fn, a[8], "cos_sin");
     const at::Tensor *qw = tensor(fn, a[9], "q_weight", true), *kw = tensor(fn, a[10], "k_weight", true);
     const double eps = number(a[11]);
-    const bool pairs = PyObject_IsTrue(a[12]) == 1;
+    const bool pairs = truth(a[12], "interleaved");
     const double k_scale = number(a[13]), v_scale = number(a[14]);
     const at::Tensor *ks = tensor(fn, a[15], "k_scales", true), *vs = tensor(fn, a[16], "v_scales", true),
                      *status = tensor(fn, a[17], "d_status", true);
@@ -201,7 +211,7 @@ int latent_append(PyObject* const* a)
                      &table = *tensor(fn, a[6], "cos_sin");
     const at::Tensor* weight = tensor(fn, a[7], "weight", true);
     const double eps = number(a[8]);
-    const bool pairs = PyObject_IsTrue(a[9]) == 1;
+    const bool pairs = truth(a[9], "interleaved");
     const at::Tensor* status = tensor(fn, a[10], "d_status", true);
     need(fn, cache.dim() == 3 && cache.is_contiguous(), "cache must be contiguous [num_blocks][B][L + R]");
     need(fn, table.scalar_type() == at::kFloat && table.dim() == 2 && table.is_contiguous(),

@@ -69,3 +69,19 @@ def test_built_anew_for_another_python_or_torch(pa, monkeypatch, tmp_path):
     os.remove(tmp_path / "key")                      # built before there was a record
     build.build_marshal()
     assert len(runs) == 3
+
+
+def test_a_flag_that_is_neither_true_nor_false_is_refused(pa):
+    t, h = torch.zeros, torch.float16
+    long = t(4, dtype=torch.int64)
+    rope = [t(4, 8, 128, dtype=h), t(4, 8, 128, dtype=h), t(4, 2, 128, dtype=h),
+            t(4, 2, 128, dtype=h), t(3, 16, 2, 128, dtype=h), t(3, 16, 2, 128, dtype=h), long, long,
+            t(10, 128)]
+    latent = [None, None, t(4, 576, dtype=h), t(3, 16, 576, dtype=h), long, long, t(10, 64)]
+    both = t(2).numpy()
+    for call, args in ((pa.pa_rope_append, rope), (pa.pa_latent_append, latent)):
+        with pytest.raises(ValueError, match="interleaved"):
+            call(*args, interleaved=both)
+        for flag in (0, 1, True, None):              # refused for the device alone
+            with pytest.raises(ValueError, match="CUDA"):
+                call(*args, interleaved=flag)
