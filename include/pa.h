@@ -625,7 +625,8 @@ PA_API pa_status pa_paged_decode_no_alloc(void* out, const void* query, const vo
  * query          [num_tokens] rows of [num_q_heads][D], query_stride elements
  *                apart; key, value likewise ([num_kv_heads][D]): slices of one
  *                fused projection are taken as they are.  Strides are
- *                multiples of 8 elements and at least a row.
+ *                multiples of 8 elements and at least a row (that of a single
+ *                token, or below of a single head, is not looked at).
  * query_out      rows as query, query_out_stride apart; may be query itself.
  * k_cache, v_cache  pools [num_blocks][block_size][num_kv_heads][D] of
  *                pool_dtype: `dtype`, PA_DTYPE_FP8_E4M3 or PA_DTYPE_INT8.

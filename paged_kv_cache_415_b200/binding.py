@@ -556,7 +556,7 @@ def pa_rope_append(query_out, query, key, value, k_cache, v_cache, slot_mapping,
                    stream=None) -> None:
     """Cache write with the norm (weights [D], optional) and the rotation of
     queries and keys on the way.  query / query_out [T][Hq][D], key / value
-    [T][Hkv][D] (any token stride; query_out may be query); pools
+    [T][Hkv][D] (any token stride of whole 16 bytes; query_out may be query); pools
     [num_blocks][B][Hkv][D] of the same type or one-byte codes (k_scale /
     v_scale, or scale pools k_scales / v_scales); slot_mapping, positions
     int64 [T]; cos_sin fp32 [max_position][rot_dim]."""
@@ -572,9 +572,9 @@ def pa_latent_append(query_out, query_rope, latent, cache, slot_mapping, positio
                      weight=None, eps=1e-6, interleaved=False, d_status=None, stream=None) -> None:
     """Write each token's latent row (normalised by `weight` [L], optional)
     and rotated key part to its slot of cache [num_blocks][B][L + R], and
-    rotate the queries' rotated part.  latent [T][L + R] (any token stride);
-    query_rope / query_out [T][H][R] views with any token and head stride, or
-    both None; cos_sin fp32 [max_position][R]."""
+    rotate the queries' rotated part.  latent [T][L + R] and query_rope /
+    query_out [T][H][R], or both None: views with any token and head stride of
+    whole 16 bytes; cos_sin fp32 [max_position][R]."""
     code = _marshal.latent_append(query_out, query_rope, latent, cache, slot_mapping, positions,
                                   cos_sin, weight, eps, interleaved, d_status,
                                   -1 if stream is None else _stream(stream))

@@ -223,10 +223,11 @@ static pa_status launch_rope_store(RopeArgs& a, pa_dtype pool, int32_t head_dim,
     return launch_rope_dim<T, PlainRows>(a, head_dim, stream);
 }
 
-// A token stride in elements: whole 16-byte vectors, at least `need`.
-static bool good_stride(int64_t stride, int64_t need, int32_t num_tokens)
+// A stride in elements between `count` rows: whole 16-byte vectors, at least
+// `need`.  That of a single row is never used and may be anything.
+static bool good_stride(int64_t stride, int64_t need, int32_t count)
 {
-    return stride % 8 == 0 && (num_tokens <= 1 || stride >= need);
+    return count <= 1 || (stride % 8 == 0 && stride >= need);
 }
 
 // ---------------------------------------------------------------------------

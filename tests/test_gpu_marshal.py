@@ -63,3 +63,31 @@ def test_other_threads_run_during_a_call(tmp_path):
         module.bind(*(address(getattr(B.LIB, "pa_" + n)) for n in names))
     B.pa_rope_append(*tensors)
     torch.cuda.synchronize()
+
+
+def test_strides_of_single_rows_do_not_matter():
+    """One token, and one head: torch gives the axis of one element whatever
+    stride a view came by, and it is not used."""
+    from paged_kv_cache_415_b200 import binding as B
+    odd = lambda t, axes: torch.as_strided(t, t.shape, [3 if i in axes else s
+                                                        for i, s in enumerate(t.stride())])
+    args = _rope_tensors(1)
+    for i in range(4):
+        args[i].normal_()
+    args[8].copy_(torch.rand_like(args[8]))
+    want = [a.clone() for a in args]
+    B.pa_rope_append(*want)
+    got = [odd(a, (0,)) if i < 4 else a for i, a in enumerate(args)]
+    B.pa_rope_append(*got)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and got[0].any()
+    h = dict(dtype=torch.bfloat16, device="cuda")
+    q, rows = torch.randn(1, 1, 64, **h), torch.randn(1, 576, **h)
+    long, table = torch.zeros(1, dtype=torch.int64, device="cuda"), torch.rand(4, 64, device="cuda")
+    outs, pools = [torch.zeros_like(q) for _ in range(2)], [torch.zeros(2, 16, 576, **h) for _ in range(2)]
+    B.pa_latent_append(outs[0], q, rows, pools[0], long, long, table)
+    B.pa_latent_append(odd(outs[1], (0, 1)), odd(q, (0, 1)), odd(rows, (0,)), pools[1], long, long,
+                       table)
+    assert torch.equal(*outs) and torch.equal(*pools) and outs[0].any()
+    with pytest.raises(B.PAError):                   # of two tokens it does
+        B.pa_latent_append(None, None, torch.as_strided(torch.zeros(1200, **h), (2, 576), (580, 1)),
+                           pools[0], long.repeat(2), long.repeat(2), table)
