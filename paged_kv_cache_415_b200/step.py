@@ -227,12 +227,14 @@ class DecodeStep:
         g.step = self                     # the scratch whose addresses it holds
         return g
 
-    def run_from_host(self, host: dict, dev: dict, scale, stream=None, fused_append=False):
+    def run_from_host(self, host: dict, dev: dict, scale, stream=None, fused_append=False,
+                      rotation=None):
         """host / dev: dicts of same-shaped tensors (pinned host / device) for
         'query', 'block_tables', 'context_lens', 'new_key', 'new_value',
-        'slot_mapping', 'block_mapping' (the last four optional) and 'out'.
-        Copies host -> device, runs the step, copies out -> host, all on
-        ``stream`` (default: the current stream)."""
+        'slot_mapping', 'block_mapping', 'positions' (the last five optional;
+        'positions' goes with a rotation) and 'out'.  Copies host -> device,
+        runs the step, copies out -> host, all on ``stream`` (default: the
+        current stream)."""
         s = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(s):
             for name, h in host.items():
@@ -241,7 +243,8 @@ class DecodeStep:
             self(dev["query"], dev["block_tables"], dev["context_lens"], scale, out=dev["out"],
                  new_key=dev.get("new_key"), new_value=dev.get("new_value"),
                  slot_mapping=dev.get("slot_mapping"), block_mapping=dev.get("block_mapping"),
-                 stream=s, fused_append=fused_append)
+                 stream=s, fused_append=fused_append, positions=dev.get("positions"),
+                 rotation=rotation)
             host["out"].copy_(dev["out"], non_blocking=True)
         return host["out"]
 
@@ -312,11 +315,16 @@ class HostPipeline:
     buffer set on that set's first use and replayed afterwards.
     """
 
-    def __init__(self, stepper: DecodeStep, dev_like: dict, device=None, use_graphs=False):
+    def __init__(self, stepper: DecodeStep, dev_like: dict, device=None, use_graphs=False,
+                 rotation=None):
         """dev_like: name -> device tensor giving the shape and dtype of each
         input ('query', 'block_tables', 'context_lens' and the optional
-        'new_key', 'new_value', 'slot_mapping', 'block_mapping') and 'out'."""
-        self.stepper = stepper
+        'new_key', 'new_value', 'slot_mapping', 'block_mapping', 'positions')
+        and 'out'.  rotation: a Rotation for every step; 'positions' is then
+        an input of each."""
+        if rotation is not None and "positions" not in dev_like:
+            raise ValueError("a rotation needs the input 'positions'")
+        self.stepper, self.rotation = stepper, rotation
         dev = device if device is not None else stepper.k_cache.device
         self.layout = {}
         off = 0
@@ -373,7 +381,8 @@ class HostPipeline:
         graph = self.graphs.get(key)
         step_args = dict(new_key=dev.get("new_key"), new_value=dev.get("new_value"),
                          slot_mapping=dev.get("slot_mapping"),
-                         block_mapping=dev.get("block_mapping"), fused_append=fused_append)
+                         block_mapping=dev.get("block_mapping"), fused_append=fused_append,
+                         positions=dev.get("positions"), rotation=self.rotation)
         if graph is not None:
             with torch.cuda.stream(self.compute), _range("pa.step"):
                 graph.replay()

@@ -69,3 +69,45 @@ def test_graphs_of_several_batch_sizes(dtype):
             graph.replay()
             assert torch.equal(out, want), turn
     assert all((t == 5).all() for t in bystanders)
+
+
+def _host(b):
+    return {k: v.cpu().pin_memory() for k, v in b.items()}
+
+
+def test_rotating_steps_fed_from_the_host():
+    """run_from_host, and HostPipeline eagerly and from graphs: what the step
+    gives on the same inputs on the device."""
+    from paged_kv_cache_415_b200.step import DecodeStep, HostPipeline, Rotation
+    dtype, seqs = torch.bfloat16, 5
+    pools = [torch.randn(32, BLOCK, HKV, D, device="cuda").to(dtype) for _ in range(2)]
+    rotation = Rotation(angle_table(64, D).cuda())
+    step = DecodeStep(*pools, seqs, HQ, 48)
+    batches = [_batch(seqs, 70 + i, dtype) for i in range(6)]
+    want = []
+    for b in batches:
+        rows = {k: v for k, v in b.items() if k not in ("query", "block_tables", "context_lens")}
+        want.append(step(b["query"], b["block_tables"], b["context_lens"], 0.1, rotation=rotation,
+                         **rows).cpu())
+    host = _host(batches[0]) | {"out": torch.empty(seqs, HQ, D, dtype=dtype).pin_memory()}
+    dev = {k: torch.empty_like(v, device="cuda") for k, v in host.items()}
+    out = step.run_from_host(host, dev, 0.1, rotation=rotation)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0])
+    like = batches[0] | {"out": batches[0]["query"]}
+    for graphs in (False, True):
+        pipe = HostPipeline(step, like, use_graphs=graphs, rotation=rotation)
+        outs = [torch.zeros(seqs, HQ, D, dtype=dtype).pin_memory() for _ in batches]
+        packed = []
+        for b in batches:
+            buf, views = pipe.host_buffer()
+            for name, t in b.items():
+                views[name].copy_(t)
+            packed.append(buf)
+        for buf, o in zip(packed, outs):
+            pipe.submit(buf, 0.1, o)
+        pipe.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want)), graphs
+    assert int(step.d_status) == 0
+    with pytest.raises(ValueError, match="positions"):
+        HostPipeline(step, {k: v for k, v in like.items() if k != "positions"}, rotation=rotation)
