@@ -272,26 +272,53 @@ class LatentDecodeStep:
 
     def __call__(self, query, block_tables, context_lens, scale, out=None, new_latent=None,
                  slot_mapping=None, positions=None, cos_sin=None, weight=None, eps=1e-6,
-                 interleaved=False, stream=None):
+                 interleaved=False, stream=None, query_rope=None, max_context_len=None):
         """query [S][H][L + R]: the absorbed part, then the part that is
-        rotated in place by the angles of `positions` when new_latent [S][L +
-        R], the step's new rows, is given (they go to slot_mapping, the latent
-        part normalised by `weight`).  Without new_latent the query is taken
-        as rotated.  Returns out [S][H][L]."""
+        rotated by the angles of `positions` when new_latent [S][L + R], the
+        step's new rows, is given (they go to slot_mapping, the latent part
+        normalised by `weight`).  The rotated part is written to query's tail;
+        it comes from query_rope [S][H][R] (any token and head stride of whole
+        16 bytes) if given, else from that tail itself, which a second step on
+        the same query would turn again.  Without new_latent the query is
+        taken as rotated.  max_context_len: a bound of this step's contexts
+        below the one given at construction.  Returns out [S][H][L]."""
+        if query_rope is not None and new_latent is None:
+            raise ValueError("query_rope is rotated along with new rows: new_latent is missing")
         with _range("pa.step"):
             if new_latent is not None:
                 tail = query[..., self.latent_dim:]
                 with _range("pa.cache_write"):
-                    B.pa_latent_append(tail, tail, new_latent, self.cache, slot_mapping, positions,
-                                       cos_sin, weight, eps, interleaved, self.d_status, stream)
+                    B.pa_latent_append(tail, tail if query_rope is None else query_rope, new_latent,
+                                       self.cache, slot_mapping, positions, cos_sin, weight, eps,
+                                       interleaved, self.d_status, stream)
             if out is None:
                 out = torch.empty(*query.shape[:2], self.latent_dim, dtype=query.dtype,
                                   device=query.device)
+            mcl = self.max_context_len if max_context_len is None else max_context_len
             with _range("pa.decode"):
-                B.pa_latent_decode(out, query, self.cache, block_tables, context_lens,
-                                   self.max_context_len, scale, self.workspace, self.d_status,
-                                   stream)
+                B.pa_latent_decode(out, query, self.cache, block_tables, context_lens, mcl, scale,
+                                   self.workspace, self.d_status, stream)
             return out
+
+    def graph(self, query, block_tables, context_lens, scale, out, new_latent=None, query_rope=None,
+              **rows):
+        """Capture one step on these device buffers, as DecodeStep.graph does.
+        A step with new rows needs query_rope, so that the eager run before the
+        capture and every replay turn the same queries once."""
+        if new_latent is not None and query_rope is None:
+            raise ValueError("a captured step rotates from query_rope, not in place")
+        args = dict(rows, out=out, new_latent=new_latent, query_rope=query_rope)
+        side = torch.cuda.Stream(device=query.device)
+        side.wait_stream(torch.cuda.current_stream(query.device))
+        with torch.cuda.stream(side):
+            self(query, block_tables, context_lens, scale, stream=side, **args)
+        torch.cuda.current_stream(query.device).wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            self(query, block_tables, context_lens, scale,
+                 stream=torch.cuda.current_stream(query.device), **args)
+        g.step = self                     # the scratch whose addresses it holds
+        return g
 
 
 class HostPipeline:

@@ -111,3 +111,47 @@ def test_rotating_steps_fed_from_the_host():
     assert int(step.d_status) == 0
     with pytest.raises(ValueError, match="positions"):
         HostPipeline(step, {k: v for k, v in like.items() if k != "positions"}, rotation=rotation)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_latent_steps_repeat(dtype):
+    """A step that rotates from query_rope can be taken again and captured:
+    the same rows and outputs each time, those of rotating in place once."""
+    from paged_kv_cache_415_b200.step import LatentDecodeStep
+    seqs, heads, lat = 4, 20, 256
+    g = torch.Generator().manual_seed(5)
+    ctx = torch.tensor([1, 16, 70, 33], dtype=torch.int32)
+    tables = torch.arange(5 * seqs, dtype=torch.int32).view(seqs, 5)
+    pool = torch.randn(24, BLOCK, lat + 64, generator=g).to(dtype).cuda()
+    p = ctx.long() - 1
+    slots = tables[torch.arange(seqs), p // BLOCK].long() * BLOCK + p % BLOCK
+    tables, ctx = tables.cuda(), ctx.cuda()
+    rows = dict(new_latent=torch.randn(seqs, lat + 64, generator=g).to(dtype).cuda(),
+                slot_mapping=slots.cuda(), positions=p.cuda(), cos_sin=angle_table(80, 64).cuda(),
+                weight=(torch.rand(lat, generator=g) + 0.5).to(dtype).cuda())
+    projected = torch.randn(seqs, heads, 192, generator=g).to(dtype).cuda()
+    turned = projected[..., 128:]                    # as the projection leaves them
+    absorbed = torch.randn(seqs, heads, lat + 64, generator=g).to(dtype).cuda()
+
+    in_place = absorbed.clone()
+    in_place[..., lat:] = turned
+    pools = [pool.clone() for _ in range(2)]
+    want = LatentDecodeStep(pools[0], seqs, heads, 80)(in_place, tables, ctx, 0.05, **rows)
+    step = LatentDecodeStep(pools[1], seqs, heads, 80)
+    query = absorbed.clone()
+    for bound in (None, 80, 70):
+        got = step(query, tables, ctx, 0.05, query_rope=turned, max_context_len=bound, **rows)
+        assert torch.equal(got, want) and torch.equal(query, in_place)
+        assert torch.equal(*pools)
+    out = torch.zeros_like(want)
+    query = absorbed.clone()
+    graph = step.graph(query, tables, ctx, 0.05, out, query_rope=turned, **rows)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want) and torch.equal(query, in_place) and torch.equal(*pools)
+    assert int(step.d_status) == 0
+    with pytest.raises(ValueError, match="query_rope"):
+        step.graph(query, tables, ctx, 0.05, out, **rows)
+    with pytest.raises(ValueError, match="new_latent"):
+        step(query, tables, ctx, 0.05, query_rope=turned)
