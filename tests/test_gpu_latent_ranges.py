@@ -3,6 +3,7 @@ hardest: maxima that move late, values of far powers of two, long pipelines."""
 import pytest
 import torch
 
+from tests.latent_cases import SCALE, point_queries, row_error, row_tolerance
 from tests.latent_reference import (F64, assert_within, attend, context_rows, latent_decode,
                                     latent_prefill)
 from tests.test_gpu_latent import _decode, _pool, _prefill, _prompt
@@ -226,3 +227,43 @@ def test_decode_minus_infinity_behind_bad_blocks(dtype, finite):
     tables[0, :4] = -1
     out = _decode(query, cache, tables, torch.tensor([ctx], dtype=torch.int32), 0.05)
     assert_within(out.cpu()[0], ref, bound, "decode")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("heads,lat,block,new,old", [
+    (3, 256, 16, [256, 130], [1150, 1999]),          # 9 to 17 tiles of keys, query tiles of unequal steps
+    (2, 512, 32, [300], [1000]),
+    (2, 512, 64, [8, 40], [4100, 2500]),             # few new tokens behind long prefixes
+    (1, 256, 8, [1500], [300]),                      # several pairs of query tiles
+])
+def test_prefill_long_pipeline(dtype, heads, lat, block, new, old):
+    """Row by row as close to 64 bits as the roundings allow: one key of
+    thousands left out or taken twice would show."""
+    x = _prompt(heads, lat, block, new, old, dtype, seed=sum(old))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = _prefill(*x, SCALE, status=status).cpu()
+    ref, bound = latent_prefill(*x, SCALE)
+    assert_within(out, ref, bound, "prefill")
+    assert float(row_error(out, ref).max()) <= row_tolerance(dtype)
+    assert int(status) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("lat,block,new,old", [(256, 16, 256, 1150), (512, 32, 200, 2200)])
+def test_prefill_every_key_at_a_border(dtype, lat, block, new, old):
+    """Queries that give nearly all their weight to a token next to a border
+    of half a tile, each such token in turn."""
+    x = _prompt(2, lat, block, [new], [old], dtype, seed=new)
+    point_queries(x, old)
+    out = _prefill(*x, SCALE).cpu()
+    ref, bound = latent_prefill(*x, SCALE)
+    assert_within(out, ref, bound, "prefill")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("heads,lat", [(128, 512), (128, 256), (65, 256)])
+def test_prefill_many_heads(dtype, heads, lat):
+    x = _prompt(heads, lat, 16, [5, 131], [0, 150], dtype, seed=heads + lat)
+    out = _prefill(*x, SCALE).cpu()
+    ref, bound = latent_prefill(*x, SCALE)
+    assert_within(out, ref, bound, "prefill")
