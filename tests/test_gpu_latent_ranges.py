@@ -267,3 +267,35 @@ def test_prefill_many_heads(dtype, heads, lat):
     out = _prefill(*x, SCALE).cpu()
     ref, bound = latent_prefill(*x, SCALE)
     assert_within(out, ref, bound, "prefill")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.06, 2.0])
+def test_prefill_scales(scale):
+    """Equal scores, a negative scale, scores in the hundreds."""
+    x = _prompt(2, 256, 16, [200, 3], [150, 140], torch.float16, 81)
+    out = _prefill(*x, scale).cpu()
+    ref, bound = latent_prefill(*x, scale)
+    assert_within(out, ref, bound, f"scale {scale}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_keeps_to_itself(dtype, value):
+    """Other heads and other queries keep every bit."""
+    g = torch.Generator().manual_seed(91)
+    cache, tables = _pool([200, 70], 16, 256, dtype, g)
+    query = torch.randn(2, 20, 320, generator=g).to(dtype)
+    ctx = torch.tensor([200, 70], dtype=torch.int32)
+    want = _decode(query, cache, tables, ctx, 0.05)
+    query[0, 3] = value
+    got = _decode(query, cache, tables, ctx, 0.05)
+    assert torch.isnan(got[0, 3]).all()
+    got[0, 3] = want[0, 3]
+    assert torch.equal(got, want)
+    x = _prompt(3, 256, 16, [150, 20], [90, 0], dtype, 92)
+    want = _prefill(*x, 0.07)
+    x[0][40, 1] = value
+    got = _prefill(*x, 0.07)
+    assert torch.isnan(got[40, 1]).all()
+    got[40, 1] = want[40, 1]
+    assert torch.equal(got, want)
