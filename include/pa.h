@@ -749,8 +749,9 @@ PA_API pa_status pa_latent_decode(void* out, const void* query, const void* cach
  * nope_dim, value_dim  128 (else PA_ERR_UNSUPPORTED).
  * workspace      at least pa_latent_prefill_workspace_size(...) bytes, 16-byte
  *                aligned: K and V of every head, 16-bit, max_context_len rows a
- *                sequence.  Contents on entry do not matter; calls that share
- *                it must not overlap.
+ *                sequence whatever the sequences' own lengths (give contexts of
+ *                very unequal lengths in several calls).  Contents on entry do
+ *                not matter; calls that share it must not overlap.
  * d_status       optional; PA_STATUS_BAD_CONTEXT: query_starts that decrease,
  *                pass num_tokens or exceed max_query_len (the sequence's rows
  *                are left as they were), a context that pa_paged_decode

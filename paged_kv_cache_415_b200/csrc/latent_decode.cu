@@ -23,8 +23,9 @@ struct LatentSplit {
     bool partials;              // whether a sequence may be cut
 };
 
-// Tiles a CTA takes at least: shorter runs cost more in partial sums than
-// they save.
+// Tiles a CTA takes at least: shorter runs cost more in partial sums than they
+// save (33 sequences to 700 tokens, 40 heads: 16.0 us a call with 2, 16.2 to 16.6
+// with 1, 20 to 22 with 3, 4 or 6; one sequence of 32773: 20.6 with 1 or 2).
 constexpr int32_t kMinTiles = 2;
 
 static LatentSplit latent_split(int32_t num_seqs, int32_t num_heads, int32_t max_context_len)

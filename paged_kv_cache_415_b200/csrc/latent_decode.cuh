@@ -31,10 +31,10 @@
 // For fp16, whose smallest numbers are near, m lies another 2^7 lower: p <= 2^15,
 // and weights down to 2^-21 of the reference keep all their bits (2^-14 without).
 //
-// Measured: 256 sequences of 3500 to 4500 tokens, 16 heads, in 204.7 us of this
+// Measured: 256 sequences of 3500 to 4500 tokens, 16 heads, in 203 us of this
 // kernel (1.20 GB, 5.9 TB/s: memory); 64 sequences to 4096 tokens, 128 heads,
-// in 95.7 us with the sum (0.42 PFLOP/s: the chain of a tile's copies, scores,
-// softmax and sums, with room for two tiles).
+// in 93 us, 97 a call with the sum (0.42 PFLOP/s: the chain of a tile's copies,
+// scores, softmax and sums, with room for two tiles).
 #pragma once
 
 #include <cuda.h>

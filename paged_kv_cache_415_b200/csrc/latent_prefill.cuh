@@ -13,9 +13,10 @@
 //
 // The expansion costs 2 L 256 operations a token and head, the attention 2 (192
 // + 128) a query, visible token and head.  Measured at 4096 new tokens, 32
-// heads, L 512: 39.2 us (0.88 PFLOP/s) and 162 us (1.06 PFLOP/s), of 1.64 that
-// products alone reach here.  The attention's products take 3480 of its 3700
-// cycles a step, as scores of 64 keys at a time read shared memory at its rate.
+// heads, L 512: 39.4 us (0.87 PFLOP/s) and 165 us (1.04 PFLOP/s), of 1.64 that
+// products alone reach here; 226 us a call, under the power limit.  The
+// attention's products take 3480 of its 3700 cycles a step, as scores of 64 keys
+// at a time read shared memory at its rate.
 //
 // Roundings: sums and softmax are fp32.  K goes to the pool's type, as the
 // queries are of it and the operands of a product are of one type.  V and the
@@ -385,8 +386,8 @@ __device__ __forceinline__ int32_t attend_size(const LatentPrefillArgs& a, int32
 
 // Grid (head, pair of query tiles of a sequence), the longest pairs first: by
 // size over all sequences where they are few enough to rank (7 prompts of 1 to
-// 700 tokens behind up to 2300, 20 heads: 97 us, in the sequences' order 107),
-// else within a sequence.  Warps:
+// 700 tokens behind up to 2300, 20 heads: 97 us, in the sequences' order 107, both
+// before tiles went in halves; now 87), else within a sequence.  Warps:
 // 0-3 and 4-7 softmax of one query tile each, a thread a query; 8 copies; 9
 // and 10 the products of one query tile each (with one warp for both the tensor
 // cores stood still 480 cycles a step).

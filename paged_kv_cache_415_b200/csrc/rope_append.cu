@@ -10,9 +10,9 @@
 //                         to query_out
 // Each reads its inputs once and writes its outputs once: both are bound by
 // memory for prompts and by launch and load latency for decode steps.
-// Measured: 8192 tokens, 32 + 32 heads of 128 in 77.5 us (5.3 TB/s), 8191
-// latent rows of 576 with 32 heads in 21.1 us (4.2 TB/s), 64 tokens of 32 + 8
-// heads in 2.05 us (from a graph).
+// Measured, a call: 8192 tokens, 32 + 32 heads of 128 in 81.6 us (5.0 TB/s; the
+// kernel alone 75.5), 8191 latent rows of 576 with 32 heads in 21.1 us (4.2 TB/s;
+// 16.5), 64 tokens of 32 + 8 heads in 2.05 us from a graph.
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math.h>
