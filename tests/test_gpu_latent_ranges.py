@@ -299,3 +299,42 @@ def test_a_query_that_is_not_finite_keeps_to_itself(dtype, value):
     assert torch.isnan(got[40, 1]).all()
     got[40, 1] = want[40, 1]
     assert torch.equal(got, want)
+
+
+def test_prompts_and_steps_on_two_streams():
+    """Prefill and decode calls side by side, each with its own workspace: the
+    bits of one after the other."""
+    from paged_kv_cache_415_b200 import binding as B
+    x = [t.cuda() for t in _prompt(16, 512, 16, [300, 70], [100, 900], torch.bfloat16, 95)]
+    query, cache, w, tables, starts, ctx = x
+    top = int(ctx.max())
+    absorbed = torch.randn(2, 16, 576, device="cuda").bfloat16()
+    outs = [torch.empty(370, 16, 128, dtype=torch.bfloat16, device="cuda"),
+            torch.empty(2, 16, 512, dtype=torch.bfloat16, device="cuda")]
+    sizes = (B.pa_latent_prefill_workspace_size(2, 16, 512, 16, top),
+             B.pa_latent_decode_workspace_size(2, 16, 512, 16, top))
+    spaces = [torch.empty(max(n, 16), dtype=torch.uint8, device="cuda") for n in sizes]
+
+    def prefill(stream=None):
+        B.pa_latent_prefill(outs[0], query, cache, w, tables, starts, ctx, 300, top, 0.07, spaces[0],
+                            stream=stream)
+
+    def decode(stream=None):
+        B.pa_latent_decode(outs[1], absorbed, cache, tables, ctx, top, 0.05, workspace=spaces[1],
+                           stream=stream)
+
+    prefill()
+    decode()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for turn in range(10):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            prefill(streams[turn % 2])
+            for _ in range(4):
+                decode(streams[1 - turn % 2])
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, r) for o, r in zip(outs, want)), turn
